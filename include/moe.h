@@ -13,6 +13,11 @@
  *                       as two grouped GEMMs over ragged per-expert row counts
  *     -> moe_combine    out[t] = sum_k w[t,k] * y_perm[pair_pos[t*K+k]] (+ shared expert row)
  *
+ * and beside it
+ *   moe_rmsnorm       the norm in front of the layer: residual addition, RMS norm, and the 8-bit
+ *                     codes that the experts read
+ *   moe_gemm_int8     the grouped int8 matrix product on its own
+ *
  * Conventions for every entry point
  *   - Pointers named as device buffers are device pointers (hipMalloc'd or torch CUDA
  *     tensors), contiguous, 16-byte aligned. Host pointers are only the config structs
@@ -63,12 +68,17 @@ typedef enum moe_status {
  *               channels); the SwiGLU output is re-quantised to MXFP8; fp32 accumulation (the
  *               MFMA applies the block scales); y_perm and y_shared are bf16, out fp32 or
  *               bf16.
+ *  MOE_INT8     x and W_r are bf16; the library quantises x to int8 for the experts with one fp32
+ *               scale per token (see moe_quantize_int8); expert weights are int8 codes with one
+ *               fp32 scale per output channel (row); int32 accumulation, exact; the SwiGLU output
+ *               is formed in fp32 and re-quantised to int8 with one scale per row; y_perm and
+ *               y_shared are bf16, out fp32 or bf16. H, I and I_shared of at most 32768.
  *
  * MX scale arrays. An operand of R rows and C channels (C a multiple of 128) has its E8M0 scale
  * codes (value 2^(code-127)) stored as [C/128][R][4] bytes: the 4-byte word at (g, r) holds the
  * scales of channels [128g + 32b, 128g + 32b + 32) of row r in byte b. Weights: one such array
  * per expert, R = the expert's output rows (2*inter for w13, H for w2), C = its input channels. */
-enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 };
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3, MOE_INT8 = 4 };
 /* Score function ("MoE 路由入门", section 3). */
 enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 };
 /* Group score for grouped top-K ("MoE 路由入门", section 7 uses the group maximum). */
@@ -90,7 +100,7 @@ typedef struct moe_config {
 } moe_config;
 
 /* Validates a config (no device access). Limits: T >= 1, 1 <= K <= E <= 256, H, I and I_shared
- * multiples of 128 for bf16/fp8, of 256 for MXFP4 and of 4 for fp32, E % n_group == 0,
+ * multiples of 128 for bf16/fp8/int8, of 256 for MXFP4 and of 4 for fp32, E % n_group == 0,
  * K <= topk_group*E/n_group, T*K < 2^31, out_dtype MOE_F32 or MOE_BF16 (MOE_F32 for fp32
  * layers). */
 moe_status moe_check_config(const moe_config* cfg);
@@ -148,10 +158,12 @@ moe_status moe_update_bias(int32_t n_experts, const int32_t* counts, float* bias
  *   pair_pos     device [P] int32 out: inverse, pair_pos[sorted_pair[i]] = i
  *   x            device [T,H] activations (fp32 / bf16 as in moe_route), or NULL to skip the gather
  *   x_perm       device [P,H] out: row i = x[sorted_pair[i] / K]; same dtype as x, except
- *                MOE_FP8_E4M3 and MOE_MXFP4 where it holds e4m3 codes (uint8)
+ *                MOE_FP8_E4M3 and MOE_MXFP4 where it holds e4m3 codes (uint8) and MOE_INT8
+ *                where it holds int8 codes
  *   x_perm_scale MOE_FP8_E4M3: device [P,H/128] fp32 out, the row scale absmax/448 of each
  *                128-channel block, code = e4m3_rne_sat(x / scale); MOE_MXFP4: device MX scale
- *                array of P rows out (the codes as moe_quantize_mx gives them); else NULL */
+ *                array of P rows out (the codes as moe_quantize_mx gives them); MOE_INT8: device
+ *                [P] fp32 out (as moe_quantize_int8 gives them); else NULL */
 moe_status moe_permute(const moe_config* cfg, const int32_t* topk_ids, int32_t* counts,
                        int32_t* offsets, int32_t* sorted_pair, int32_t* pair_pos, const void* x,
                        void* x_perm, void* x_perm_scale, void* ws, size_t ws_bytes, void* stream);
@@ -180,19 +192,23 @@ moe_status moe_permute_noalloc(const moe_config* cfg, const int32_t* topk_ids, i
  *   n_rows     rows of x_rows and y_rows (P for routed, T for shared); offsets[n_experts] = n_rows
  *   inter      intermediate size of these experts (cfg->I or cfg->I_shared)
  *   offsets    device [n_experts+1] int32: rows [offsets[e], offsets[e+1]) belong to expert e
- *   x_rows     device [n_rows,H]: fp32 / bf16, or e4m3 codes (MOE_FP8_E4M3, MOE_MXFP4)
+ *   x_rows     device [n_rows,H]: fp32 / bf16, or e4m3 codes (MOE_FP8_E4M3, MOE_MXFP4), or int8
+ *              codes (MOE_INT8)
  *   x_scale    MOE_FP8_E4M3: device [n_rows,H/128] fp32 row-block scales; MOE_MXFP4: device MX
- *              scale array of n_rows rows; else NULL
+ *              scale array of n_rows rows; MOE_INT8: device [n_rows] fp32; else NULL
  *   w13        device [n_experts, 2*inter, H]: gate rows [0,inter), up rows [inter,2*inter);
  *              MOE_MXFP4: [n_experts, 2*inter, H/2] bytes of packed e2m1 codes
  *   w13_scale  MOE_FP8_E4M3: device [n_experts, 2*inter/128, H/128] fp32; MOE_MXFP4: device
- *              [n_experts] MX scale arrays of 2*inter rows and H channels; else NULL
+ *              [n_experts] MX scale arrays of 2*inter rows and H channels; MOE_INT8: device
+ *              [n_experts, 2*inter] fp32; else NULL
  *   w2         device [n_experts, H, inter] (MOE_MXFP4: [n_experts, H, inter/2] packed e2m1)
  *   w2_scale   MOE_FP8_E4M3: device [n_experts, H/128, inter/128] fp32; MOE_MXFP4: device
- *              [n_experts] MX scale arrays of H rows and inter channels; else NULL
- *   y_rows     device [n_rows,H] out: fp32 (MOE_F32) or bf16 (MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4)
+ *              [n_experts] MX scale arrays of H rows and inter channels; MOE_INT8: device
+ *              [n_experts, H] fp32; else NULL
+ *   y_rows     device [n_rows,H] out: fp32 (MOE_F32) or bf16 (every other type)
  * The SwiGLU output is kept in the workspace (bf16, fp32 for MOE_F32, e4m3 + scales for fp8 and
- * MX). */
+ * MX, fp32 and int8 + scales for MOE_INT8). MOE_INT8 layers clamp the offsets they read to
+ * [0, n_rows]. */
 moe_status moe_expert_ffn(const moe_config* cfg, int32_t n_experts, int32_t n_rows, int32_t inter,
                           const int32_t* offsets, const void* x_rows, const void* x_scale,
                           const void* w13, const void* w13_scale, const void* w2,
@@ -208,9 +224,9 @@ moe_status moe_expert_ffn(const moe_config* cfg, int32_t n_experts, int32_t n_ro
  *               outside is clamped to the last token, so no read leaves x)
  *   x           device [T,H]: fp32 / bf16, or e4m3 codes (MOE_FP8_E4M3 / MOE_MXFP4, e.g.
  *               moe_quantize_fp8 / moe_quantize_mx of the layer input, the same codes the shared
- *               expert reads)
+ *               expert reads), or int8 codes (MOE_INT8, moe_quantize_int8 or moe_rmsnorm)
  *   x_scale     MOE_FP8_E4M3: device [T,H/128] fp32; MOE_MXFP4: device MX scale array of T
- *               rows; else NULL
+ *               rows; MOE_INT8: device [T] fp32; else NULL
  * Other arguments, outputs and errors as moe_expert_ffn; MOE_ERR_UNSUPPORTED if x is 4 GiB or
  * more (the per-row offsets are 32-bit). */
 moe_status moe_expert_ffn_gather(const moe_config* cfg, int32_t n_experts, int32_t n_rows,
@@ -289,6 +305,68 @@ moe_status moe_quantize_fp8(int32_t rows, int32_t cols, const void* in, uint8_t*
  *   of `rows` rows out ([cols/128][rows][4] bytes). cols must be a positive multiple of 128. */
 moe_status moe_quantize_mx(int32_t rows, int32_t cols, const void* in, uint8_t* codes,
                            uint8_t* scales, void* stream);
+
+/* moe_quantize_int8 -- int8 row quantisation of bf16 rows (the experts' input in the int8 layer):
+ * per row, scale = absmax/127 (fp32), code = v/scale rounded to nearest even (an IEEE fp32
+ * quotient), within +-127; an all-zero row gets scale 0 and codes 0; a row with a NaN or an
+ * infinity gets a NaN or infinite scale and codes 0, so that its products are NaN.
+ *   in device [rows,cols] bf16; codes device [rows,cols] int8 out; scales device [rows] fp32 out.
+ *   cols must be a positive multiple of 128, at most 32768. */
+moe_status moe_quantize_int8(int32_t rows, int32_t cols, const void* in, int8_t* codes, float* scales, void* stream);
+
+/* Shape and types of a moe_rmsnorm call. Strides are elements from one row to the next, 0 = cols
+ * (contiguous); rows need only their element's alignment. */
+typedef struct moe_norm_config {
+  int32_t rows, cols;            /* rows >= 0 (0: nothing happens), 1 <= cols <= 32768 */
+  int32_t x_dtype;               /* MOE_F32 | MOE_BF16, as the other three types */
+  int32_t residual_dtype;        /* of residual and residual_out */
+  int32_t weight_dtype;
+  int32_t y_dtype;
+  int32_t quant;                 /* 0: no codes; MOE_FP8_E4M3, MOE_MXFP4 or MOE_INT8: codes as the
+                                    experts of that layer type read them (cols a multiple of 128) */
+  float eps;                     /* finite, >= 0 */
+  int64_t x_stride, residual_stride, residual_out_stride, y_stride;
+} moe_norm_config;
+
+/* moe_rmsnorm -- residual addition, RMS norm and an optional 8-bit output, in one pass over the
+ * rows: the step in front of a MoE layer (n feeds the router as y and the experts as codes).
+ *   s = x + residual,  n[c] = s[c] * weight[c] / sqrt(mean(s^2) + eps)   in fp32, per row
+ *   x            device [rows,cols] fp32 or bf16
+ *   weight       device [cols] fp32 or bf16
+ *   residual     device [rows,cols] fp32 or bf16, or NULL (s = x)
+ *   residual_out device [rows,cols] out: s rounded once to residual_dtype, or NULL; may be
+ *                `residual` itself with the same stride
+ *   y            device [rows,cols] out: n rounded once to y_dtype, or NULL when there are codes;
+ *                may be x itself with the same type and stride
+ *   codes        quant != 0: device [rows,cols] contiguous out: e4m3 codes (uint8) or int8 codes of
+ *                n (of the fp32 value, not of the rounded y), as moe_quantize_fp8 / _mx / _int8
+ *                define them; else NULL
+ *   scales       quant != 0: out, MOE_FP8_E4M3 device [rows,cols/128] fp32, MOE_MXFP4 device MX
+ *                scale array of `rows` rows (the code 255, NaN, for a block that holds a NaN or
+ *                an infinity), MOE_INT8 device [rows] fp32; else NULL
+ * Outputs overlap nothing else. The sum of squares is fp32: |s| up to 1.8e19 / sqrt(cols). eps = 0
+ * on an all-zero row gives NaN, as the formula does. */
+moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* weight, const void* residual,
+                       void* residual_out, void* y, void* codes, void* scales, void* stream);
+
+/* moe_gemm_int8 -- grouped int8 matrix product with a scale per token and per output channel:
+ *   y[i][n] = (sum_k x[i][k] * w[e(i)][n][k]) * x_scale[i] * w_scale[e(i)][n]
+ * the sum exact in int32, then fp32, rounded once to y's type. n_experts = 1 is the dense product.
+ *   n_rows     rows of x and y
+ *   offsets    device [n_experts+1] int32: rows [offsets[e], offsets[e+1]) take expert e's weights
+ *              (values are clamped to [0, n_rows]; ascending, else rows are written twice); rows
+ *              in no group are left as they were. NULL with n_experts = 1: every row
+ *   x          device [n_rows,K] int8;       x_scale device [n_rows] fp32
+ *   w          device [n_experts,N,K] int8;  w_scale device [n_experts,N] fp32
+ *   y          device [n_rows,N] out, of type y_dtype (MOE_F32 or MOE_BF16)
+ *   ws         device workspace of moe_gemm_int8_workspace_size() bytes, one call at a time; needs no
+ *              initialisation
+ * Any N up to 2^20; K a multiple of 16, at most 131071 (MOE_ERR_UNSUPPORTED otherwise);
+ * n_experts*N*K is not limited, N*K is below 2^31. x, w, w_scale, y and ws are 16-byte aligned. */
+size_t moe_gemm_int8_workspace_size(void);
+moe_status moe_gemm_int8(int32_t n_experts, int32_t n_rows, int32_t N, int32_t K, const int32_t* offsets, const int8_t* x,
+                         const float* x_scale, const int8_t* w, const float* w_scale, void* y, int32_t y_dtype, void* ws,
+                         size_t ws_bytes, void* stream);
 
 /* Reads (and clears) the device error word kept at the start of `ws`, waiting for `stream`.
  * *code = 0 when no kernel flagged bad data since the last read; otherwise the returned

@@ -27,7 +27,7 @@ class LayerConfig:
     topk_group: int      # groups kept per token
     group_rule: str      # "top2_sum" | "max"
     bias: Optional[str]  # None | "normal" (std 0.1) | "zipf" (skew calibrated to Zipf s=1.2)
-    dtype: str           # "f32" | "bf16" | "fp8" | "mxfp4" (MXFP8 activations x MXFP4 weights)
+    dtype: str           # "f32" | "bf16" | "fp8" | "mxfp4" (MXFP8 activations x MXFP4 weights) | "int8"
     I_shared: int        # shared expert intermediate size (0 = none)
     seed: int
     out: str = "bf16"    # type of the layer output: "f32" | "bf16" (fp32 layers: "f32")
@@ -62,6 +62,17 @@ CONFIGS = {
     8: LayerConfig("decode-zipf-mxfp4", T=128, H=7168, I=2048, E=256, K=8, score="sigmoid",
                    renorm=True, route_scale=2.5, n_group=8, topk_group=4, group_rule="top2_sum",
                    bias="zipf", dtype="mxfp4", I_shared=2048, seed=7),
+}
+
+
+# int8 layers (one scale per token, one per output channel) on the fine-grained shapes.
+INT8_CONFIGS = {
+    9: LayerConfig("dsv3-int8", T=8192, H=7168, I=2048, E=256, K=8, score="sigmoid",
+                   renorm=True, route_scale=2.5, n_group=8, topk_group=4, group_rule="top2_sum",
+                   bias="normal", dtype="int8", I_shared=2048, seed=8),
+    10: LayerConfig("decode-zipf-int8", T=128, H=7168, I=2048, E=256, K=8, score="sigmoid",
+                    renorm=True, route_scale=2.5, n_group=8, topk_group=4, group_rule="top2_sum",
+                    bias="zipf", dtype="int8", I_shared=2048, seed=9),
 }
 
 

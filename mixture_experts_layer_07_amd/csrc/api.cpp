@@ -102,6 +102,9 @@ using namespace moe;
     if (_e != hipSuccess) return fail_hip(_e, where); \
   } while (0)
 
+// Layer types whose experts read codes and scales.
+static bool quantised(int dtype) { return dtype == MOE_FP8_E4M3 || dtype == MOE_MXFP4 || dtype == MOE_INT8; }
+
 static moe_status checked_config(const moe_config* cfg) {
   std::string why;
   moe_status s = check_config(cfg, &why);
@@ -178,11 +181,11 @@ static moe_status permute_args(const char* where, const moe_config* cfg, const i
     return fail(MOE_ERR_INVALID_ARG, w + ": NULL buffer");
   if ((x == nullptr) != (x_perm == nullptr))
     return fail(MOE_ERR_INVALID_ARG, w + ": x and x_perm must both be given or both NULL");
-  const bool quant = c.dtype == MOE_FP8_E4M3 || c.dtype == MOE_MXFP4;
+  const bool quant = quantised(c.dtype);
   if (x && quant && !x_perm_scale)
-    return fail(MOE_ERR_INVALID_ARG, w + ": fp8 and MX layers need x_perm_scale");
+    return fail(MOE_ERR_INVALID_ARG, w + ": fp8, MX and int8 layers need x_perm_scale");
   if (!quant && x_perm_scale)
-    return fail(MOE_ERR_INVALID_ARG, w + ": x_perm_scale is only for fp8 and MX layers");
+    return fail(MOE_ERR_INVALID_ARG, w + ": x_perm_scale is only for fp8, MX and int8 layers");
   return MOE_OK;
 }
 
@@ -266,11 +269,11 @@ static moe_status expert_ffn(const char* where, const moe_config* cfg, int32_t n
     return fail(MOE_ERR_INVALID_ARG, w + ": inter must be in [1, max(I, I_shared)] and a multiple of " +
                                          std::to_string(q));
   if (!offsets || !x || !w13 || !w2 || !y_rows) return fail(MOE_ERR_INVALID_ARG, w + ": NULL buffer");
-  const bool quant = c.dtype == MOE_FP8_E4M3 || c.dtype == MOE_MXFP4;
+  const bool quant = quantised(c.dtype);
   if (quant && (!x_scale || !w13_scale || !w2_scale))
-    return fail(MOE_ERR_INVALID_ARG, w + ": fp8 and MX layers need x_scale, w13_scale, w2_scale");
+    return fail(MOE_ERR_INVALID_ARG, w + ": fp8, MX and int8 layers need x_scale, w13_scale, w2_scale");
   if (!quant && (x_scale || w13_scale || w2_scale))
-    return fail(MOE_ERR_INVALID_ARG, w + ": scales are only for fp8 and MX layers");
+    return fail(MOE_ERR_INVALID_ARG, w + ": scales are only for fp8, MX and int8 layers");
   if (gather) {
     const int64_t xb = c.dtype == MOE_F32 ? 4 : (quant ? 1 : 2);
     if ((int64_t)c.T * c.H * xb >= (int64_t(1) << 32))
@@ -299,10 +302,13 @@ static moe_status expert_ffn(const char* where, const moe_config* cfg, int32_t n
   a.y = y_rows;
   a.h = at<void>(ws, L.h);
   a.h_scale = quant ? at<void>(ws, L.hscale) : nullptr;
+  a.h_codes = c.dtype == MOE_INT8 ? at<void>(ws, L.hq) : nullptr;
   a.x_scale_grouped = quant ? at<void>(ws, L.xscale) : nullptr;
   a.tiles = at<int32_t>(ws, L.tiles);
   a.part = at<float>(ws, L.part);
-  MOE_HIP(launch_expert_ffn(a, static_cast<hipStream_t>(stream)), "expert_ffn");
+  MOE_HIP(c.dtype == MOE_INT8 ? launch_expert_ffn_int8(a, static_cast<hipStream_t>(stream))
+                              : launch_expert_ffn(a, static_cast<hipStream_t>(stream)),
+          "expert_ffn");
   return MOE_OK;
 }
 
@@ -427,6 +433,99 @@ moe_status moe_quantize_mx(int32_t rows, int32_t cols, const void* in, uint8_t* 
   MOE_TRY(ensure_device());
   MOE_HIP(launch_quantize_mx(rows, cols, in, codes, scales, static_cast<hipStream_t>(stream)),
           "quantize_mx");
+  return MOE_OK;
+}
+
+moe_status moe_quantize_int8(int32_t rows, int32_t cols, const void* in, int8_t* codes, float* scales, void* stream) {
+  if (rows < 0 || cols < 128 || cols % 128)
+    return fail(MOE_ERR_INVALID_ARG, "moe_quantize_int8: rows >= 0, cols a positive multiple of 128");
+  if (cols > kMaxRowCols) return fail(MOE_ERR_UNSUPPORTED, "moe_quantize_int8: cols above 32768 is not supported");
+  if (!in || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "moe_quantize_int8: NULL buffer");
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(ensure_device());
+  MOE_HIP(launch_quantize_int8("quantize_int8", in, false, rows, rows, nullptr, 1, cols, codes, scales,
+                               static_cast<hipStream_t>(stream)),
+          "quantize_int8");
+  return MOE_OK;
+}
+
+moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* weight, const void* residual,
+                       void* residual_out, void* y, void* codes, void* scales, void* stream) {
+  std::string why;
+  const moe_status cs = check_norm(cfg, &why);
+  if (cs != MOE_OK) return fail(cs, "moe_rmsnorm: " + why);
+  const moe_norm_config& c = *cfg;
+  if (!x || !weight) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: NULL buffer");
+  if (residual_out && !residual) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: residual_out needs residual");
+  if (c.quant != 0 ? (!codes || !scales) : (codes || scales))
+    return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: codes and scales go with quant");
+  if (!y && !codes) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: no output (y or codes)");
+  if (reinterpret_cast<uintptr_t>(codes) % 8 || reinterpret_cast<uintptr_t>(scales) % 4)
+    return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: codes and scales must be 8- and 4-byte aligned");
+  if (c.rows == 0) return MOE_OK;
+  MOE_TRY(ensure_device());
+  NormArgs a;
+  a.x = x;
+  a.g = weight;
+  a.r = residual;
+  a.r_out = residual_out;
+  a.y = y;
+  a.codes = codes;
+  a.scales = scales;
+  auto bytes = [&](int64_t stride, int32_t dtype) { return (stride ? stride : c.cols) * (dtype == MOE_F32 ? 4 : 2); };
+  a.x_bytes = bytes(c.x_stride, c.x_dtype);
+  a.r_bytes = bytes(c.residual_stride, c.residual_dtype);
+  a.ro_bytes = bytes(c.residual_out_stride, c.residual_dtype);
+  a.y_bytes = bytes(c.y_stride, c.y_dtype);
+  a.rows = c.rows;
+  a.cols = c.cols;
+  a.eps = c.eps;
+  a.x_f32 = c.x_dtype == MOE_F32;
+  a.r_f32 = c.residual_dtype == MOE_F32;
+  a.y_f32 = c.y_dtype == MOE_F32;
+  a.g_f32 = c.weight_dtype == MOE_F32;
+  MOE_HIP(launch_rmsnorm(a, c.quant, static_cast<hipStream_t>(stream)), "rmsnorm");
+  return MOE_OK;
+}
+
+size_t moe_gemm_int8_workspace_size(void) { return (size_t)kTileMetaInts * 4 + kInt8PartBytes; }
+
+moe_status moe_gemm_int8(int32_t n_experts, int32_t n_rows, int32_t N, int32_t K, const int32_t* offsets, const int8_t* x,
+                         const float* x_scale, const int8_t* w, const float* w_scale, void* y, int32_t y_dtype, void* ws,
+                         size_t ws_bytes, void* stream) {
+  if (n_experts < 1 || n_experts > kMaxExperts)
+    return fail(MOE_ERR_INVALID_ARG, "moe_gemm_int8: n_experts must be in [1, 256]");
+  if (n_rows < 0 || N < 1 || K < 1) return fail(MOE_ERR_INVALID_ARG, "moe_gemm_int8: n_rows >= 0, N and K positive");
+  if (y_dtype != MOE_F32 && y_dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "moe_gemm_int8: y_dtype must be MOE_F32 or MOE_BF16");
+  if (K % 16) return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: K must be a multiple of 16");
+  if (K > kMaxInt8K) return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: K above 131071 could overflow the int32 sums");
+  if ((int64_t)N * K >= (int64_t(1) << 31) || N > (1 << 20))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: N above 2^20 or one expert of 2^31 codes is not supported");
+  if (!x || !x_scale || !w || !w_scale || !y || (!offsets && n_experts > 1))
+    return fail(MOE_ERR_INVALID_ARG, "moe_gemm_int8: NULL buffer");
+  if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if (ws_bytes < moe_gemm_int8_workspace_size())
+    return fail(MOE_ERR_WORKSPACE, "workspace smaller than moe_gemm_int8_workspace_size()");
+  for (const void* p : {(const void*)x, (const void*)w, (const void*)w_scale, (const void*)y, (const void*)ws})
+    if (reinterpret_cast<uintptr_t>(p) % 16) return fail(MOE_ERR_INVALID_ARG, "moe_gemm_int8: buffers must be 16-byte aligned");
+  if (n_rows == 0) return MOE_OK;
+  MOE_TRY(ensure_device());
+  Int8GemmArgs a;
+  a.n_exp = n_experts;
+  a.n_rows = n_rows;
+  a.N = N;
+  a.K = K;
+  a.offsets = offsets;
+  a.x = x;
+  a.x_scale = x_scale;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.y = y;
+  a.y_f32 = y_dtype == MOE_F32;
+  a.tiles = static_cast<int32_t*>(ws);
+  a.part = at<float>(ws, (size_t)kTileMetaInts * 4);
+  MOE_HIP(launch_int8_gemm(a, static_cast<hipStream_t>(stream)), "gemm_int8");
   return MOE_OK;
 }
 

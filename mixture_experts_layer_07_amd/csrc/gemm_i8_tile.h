@@ -1,0 +1,292 @@
+// Tile machinery of the int8 grouped products on MFMA 32x32x32 (int32 accumulate): y = (x . w^T)
+// with a scale per token (row of x) and per output channel (row of w).
+//
+// A K step is 128 bytes of every row, 128 channels here, so the LDS stages, the direct-to-LDS loads
+// and the step's schedule are those of the bf16 tiles (gemm_bf16_tile.h); each MFMA retires twice
+// the products. Scales that are constant along K never enter the loop: int32 sums are exact for
+// K <= 131071 (|code| <= 128), and one multiplication by each scale in the epilogue finishes them.
+//
+// The MFMAs take the weights as their first operand (the transposed product): a lane then holds one
+// token and runs of four consecutive output channels, so its token scale is one value per block and
+// its outputs leave as 8- or 16-byte stores.
+//
+// K need not fill the steps. KT = 2 ceil(K / 256) steps are run; a lane's 16-byte chunk past K is
+// read at its last place inside the row instead (one min per step), and the weights of such chunks
+// are written to the LDS as zeros, so what stands in x there adds nothing.
+#pragma once
+
+#include "gemm_bf16_tile.h"
+
+namespace moe {
+
+typedef __attribute__((__vector_size__(16 * sizeof(int)))) int i32x16;
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4;
+
+namespace w4 {
+template <int MB, int NB>
+__device__ __forceinline__ void frags(const u32x4* sa, const u32x4* sb, int ks, int r0, int c0, int lane,
+                                      i32x4 (&a)[MB], i32x4 (&b)[NB]) {
+  const int lrow = lane & 31, lk = lane >> 5;
+  const int slot = (ks * 2 + lk) ^ lds_swz(lrow);  // block rows start at multiples of 32
+  const u32x4* la = sa + (r0 + lrow) * 8 + slot;
+  const u32x4* lb = sb + (c0 + lrow) * 8 + slot;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) a[mb] = __builtin_bit_cast(i32x4, la[mb * 256]);
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) b[nb] = __builtin_bit_cast(i32x4, lb[nb * 256]);
+}
+
+template <int MB, int NB>
+__device__ __forceinline__ void mfmas(i32x16 (&acc)[MB][NB], const i32x4 (&a)[MB], const i32x4 (&b)[NB]) {
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      acc[mb][nb] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[nb], a[mb], acc[mb][nb], 0, 0, 0);
+}
+}  // namespace w4
+
+namespace i8 {
+// Partial tiles of K pieces: int32 sums, exact in any order.
+template <int MB, int NB>
+__device__ __forceinline__ void store_partial(float* part, const i32x16 (&acc)[MB][NB], int tid) {
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const i32x4 v = {acc[mb][nb][4 * c], acc[mb][nb][4 * c + 1], acc[mb][nb][4 * c + 2], acc[mb][nb][4 * c + 3]};
+        reinterpret_cast<i32x4*>(part)[((mb * NB + nb) * 4 + c) * 256 + tid] = v;
+      }
+}
+template <int MB, int NB>
+__device__ __forceinline__ void add_partial(const float* part, i32x16 (&acc)[MB][NB], int tid) {
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const i32x4 v = reinterpret_cast<const i32x4*>(part)[((mb * NB + nb) * 4 + c) * 256 + tid];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mb][nb][4 * c + e] += v[e];
+      }
+}
+
+// Scales of the four consecutive channels n .. n + 3 of an expert of Nb channels (clamped; the
+// extra ones are never stored). vec: Nb is a multiple of 4, so the four are one 16-byte load.
+__device__ __forceinline__ f32x4 channel_scales(const float* sw, int n, int Nb, bool vec) {
+  if (vec) return *reinterpret_cast<const f32x4*>(sw + (n < Nb ? n : 0));
+  f32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = sw[n + j < Nb ? n + j : Nb - 1];
+  return v;
+}
+
+// Epilogue of a wave's MB x NB blocks at rows r0.., weight rows c0.. of the 256-row weight tile. In a
+// 32x32 block lane l holds token l & 31, channels 8 (i / 4) + 4 (l / 32) + i % 4.
+// The int32 sum is rounded to fp32 (2^-24 of it) and multiplied by the two scales in fp32.
+// GLU: blocks 2q, 2q+1 hold gate and up of the same channels; SiLU(gate) * up is kept in fp32. (It is
+// requantised per row next. A value rounded to bf16 first would cross a rounding border of the int8
+// grid in a share of cases that costs about 0.7 % of rms in Linear-2's output, four times what
+// the output's own bf16 rounding does.)
+// Else: y rows, bf16 (rounded once) or fp32.
+template <int MB, int NB, bool GLU, bool OUTF32>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, const i32x16 (&acc)[MB][NB],
+                                         const float* s_xs, int r0, int c0, int lane) {
+  const int lrow = lane & 31, lk = lane >> 5;
+  const int ldc = (int)g.ldc;
+  const int row0 = __builtin_amdgcn_readfirstlane(ti.row0), mvalid = __builtin_amdgcn_readfirstlane(ti.mvalid);
+  const __amdgpu_buffer_rsrc_t rc =
+      __builtin_amdgcn_make_buffer_rsrc(g.C + (size_t)row0 * g.ldc, (short)0, mvalid * ldc, 0x00020000);
+  const float* sw = g.b_scale + (size_t)ti.e * g.b_scale_exp;
+  int rbase = r0 + lrow;
+  asm volatile("" : "+v"(rbase));  // (row offsets formed here, not held across the K loop)
+  if constexpr (GLU) {
+#pragma unroll
+    for (int q = 0; q < NB / 2; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = ti.nt * 128 + c0 / 2 + q * 32 + j * 8 + lk * 4;
+        const f32x4 sg = *reinterpret_cast<const f32x4*>(sw + n);
+        const f32x4 su = *reinterpret_cast<const f32x4*>(sw + g.glu_I + n);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const float sx = s_xs[rbase + mb * 32];
+          u32x4 h;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float gate = (float)acc[mb][2 * q][4 * j + i] * (sx * sg[i]);
+            const float up = (float)acc[mb][2 * q + 1][4 * j + i] * (sx * su[i]);
+            h[i] = __float_as_uint(silu_fast(gate) * up);
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(h, rc, (rbase + mb * 32) * ldc + n * 4, 0, 0);
+        }
+      }
+  } else {
+    const bool vec = (g.N_out & 3) == 0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = ti.nt * 256 + c0 + nb * 32 + j * 8 + lk * 4;
+        const f32x4 sn = channel_scales(sw, n, g.N_out, vec);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          const float sx = s_xs[rbase + mb * 32];
+          float v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = (float)acc[mb][nb][4 * j + i] * (sx * sn[i]);
+          const int off = (rbase + mb * 32) * ldc + n * (OUTF32 ? 4 : 2);
+          if (vec) {
+            if (n < g.N_out) {
+              if constexpr (OUTF32) {
+                const u32x4 u = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+                __builtin_amdgcn_raw_buffer_store_b128(u, rc, off, 0, 0);
+              } else {
+                typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+                const u32x2 u = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+                __builtin_amdgcn_raw_buffer_store_b64(u, rc, off, 0, 0);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (n + i < g.N_out) {
+                if constexpr (OUTF32)
+                  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), rc, off + i * 4, 0, 0);
+                else
+                  __builtin_amdgcn_raw_buffer_store_b16((short)(bf16x2(v[i], 0.f) & 0xFFFF), rc, off + i * 2, 0, 0);
+              }
+          }
+        }
+      }
+  }
+}
+}  // namespace i8
+
+// The loads of the bf16 tiles with the lane's K offset held inside its row (kmax: the last offset at
+// which the lane's chunk is inside, a multiple of 128 or, in rows shorter than the chunk's place,
+// the negative offset that reads the row's first chunk).
+#define MOE_I8_KOFF(kk) ((uint32_t)min((int)(kk) * 128, kmax))
+#define MOE_I8_ALOADS(stage, kk, AJ_)                                                            \
+  do {                                                                                           \
+    const uint32_t ko_ = MOE_I8_KOFF(kk);                                                        \
+    _Pragma("unroll") for (int j_ = 0; j_ < (AJ_); ++j_)                                         \
+        dma_to_lds<16>(Ab + (uint32_t)(oa[j_] + ko_), (stage) + la_off[j_]);                    \
+  } while (0)
+#define MOE_I8_BLOAD(R, kk, J0, J1)                                                              \
+  do {                                                                                           \
+    const uint32_t ko_ = MOE_I8_KOFF(kk);                                                        \
+    _Pragma("unroll") for (int j_ = (J0); j_ < (J1); ++j_) {                                     \
+      uint32_t o_ = ob[j_];                                                                      \
+      asm volatile("" : "+v"(o_));                                                               \
+      R[j_] = *reinterpret_cast<const u32x4*>(Be + (uint32_t)(o_ + ko_));                        \
+    }                                                                                            \
+  } while (0)
+#define MOE_I8_BDMA(stage, kk)                                                                   \
+  do {                                                                                           \
+    const uint32_t ko_ = MOE_I8_KOFF(kk);                                                        \
+    _Pragma("unroll") for (int j_ = 0; j_ < 8; ++j_)                                             \
+        dma_to_lds<16>(Be + (uint32_t)(ob[j_] + ko_), (stage) + j_ * 256 + wave * 64);           \
+  } while (0)
+// Zeros instead of this lane's weights of step kk where its chunk lies past K.
+#define MOE_I8_MASK(R, kk)                                                                       \
+  do {                                                                                           \
+    if ((int)(kk) * 128 > kmax) {                                                                \
+      _Pragma("unroll") for (int j_ = 0; j_ < 8; ++j_) R[j_] = u32x4{0u, 0u, 0u, 0u};            \
+    }                                                                                            \
+  } while (0)
+
+// One step on stage (ca, cb), as MOE_W4_STEP with the loads above.
+#define MOE_I8_STEP(MB_, NB_, ca, cb, na, nb, k, LB, W, NEXT, RW, RL)                           \
+  w4::frags<MB_, NB_>(ca, cb, 1, r0, c0, lane, a1, b1);                                          \
+  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 0, 3);                                                       \
+  w4::mfmas<MB_, NB_>(acc, a0, b0);                                                              \
+  MOE_W4_SUBL(MB_, NB_, LB, 3)                                                                   \
+  w4::frags<MB_, NB_>(ca, cb, 2, r0, c0, lane, a0, b0);                                          \
+  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 3, 6);                                                       \
+  w4::mfmas<MB_, NB_>(acc, a1, b1);                                                              \
+  MOE_W4_SUBL(MB_, NB_, LB, 3)                                                                   \
+  w4::frags<MB_, NB_>(ca, cb, 3, r0, c0, lane, a1, b1);                                          \
+  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 6, 8);                                                       \
+  w4::mfmas<MB_, NB_>(acc, a0, b0);                                                              \
+  MOE_W4_SUBL(MB_, NB_, LB, 2)                                                                   \
+  /* own fragment reads and weight writes done, A of step k+1 landed (only this step's weight \
+     loads may be outstanding); the barrier extends both to all waves */                       \
+  __builtin_amdgcn_s_waitcnt((LB) ? kWaitLgkm0Vm8 : kWaitLgkm0Vm0);                              \
+  __builtin_amdgcn_s_barrier();                                                                  \
+  __builtin_amdgcn_sched_barrier(0);                                                             \
+  if (NEXT) w4::frags<MB_, NB_>(na, nb, 0, r0, c0, lane, a0, b0);                                \
+  if (W) {                                                                                       \
+    MOE_W4_BWRITE(cb, RW);                                                                       \
+    MOE_I8_ALOADS(ca, (k) + 2, AJ);                                                              \
+  }                                                                                              \
+  w4::mfmas<MB_, NB_>(acc, a1, b1);                                                              \
+  MOE_W4_POST(MB_, NB_, W, NEXT)                                                                 \
+  __builtin_amdgcn_sched_barrier(0);
+
+// One tile (or K piece of a tile) with waves of MB x NB blocks: rows r0.., weight rows c0... tail:
+// whether steps [k0, k1) reach past the K / 128 full steps (uniform; then at most the last two do).
+#define MOE_I8_TILE(MB_, NB_, r0_, c0_, SPLIT)                                                   \
+  {                                                                                              \
+    const int r0 = (r0_), c0 = (c0_);                                                            \
+    constexpr int AJ = (MB_) * (NB_) == 16 ? 8 : (MB_); /* A load instructions per wave, step */ \
+    i32x16 acc[MB_][NB_];                                                                        \
+    _Pragma("unroll") for (int mb = 0; mb < (MB_); ++mb)                                         \
+      _Pragma("unroll") for (int nb = 0; nb < (NB_); ++nb)                                       \
+        _Pragma("unroll") for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0;                       \
+    u32x4 RB0[8], RB1[8];                                                                        \
+    MOE_I8_ALOADS(sA0, k0, AJ);                                                                  \
+    MOE_I8_BDMA(sB0, k0);                                                                        \
+    MOE_I8_ALOADS(sA1, k0 + 1, AJ);                                                              \
+    MOE_I8_BDMA(sB1, k0 + 1);                                                                    \
+    /* (a two-step tile loads step k0+1 again: unused, keeps the wait count fixed) */           \
+    MOE_I8_BLOAD(RB0, k0 + 2 < k1 ? k0 + 2 : k1 - 1, 0, 8);                                      \
+    if (tail && k0 + 2 == k1) {                                                                  \
+      /* both steps came by direct-to-LDS loads: zeros over this lane's chunks past K */         \
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0Vm0);                                                 \
+      const u32x4 z_ = {0u, 0u, 0u, 0u};                                                         \
+      _Pragma("unroll") for (int j_ = 0; j_ < 8; ++j_) {                                         \
+        if (k0 * 128 > kmax) sB0[bw_off + j_ * 256] = z_;                                        \
+        if ((k0 + 1) * 128 > kmax) sB1[bw_off + j_ * 256] = z_;                                  \
+      }                                                                                          \
+      __syncthreads();                                                                           \
+    }                                                                                            \
+    /* step k0 landed (step k0+1 and the weights of k0+2 may still be in flight) */             \
+    __builtin_amdgcn_s_waitcnt(wait_lgkm0_vm(AJ + 16));                                          \
+    __builtin_amdgcn_s_barrier();                                                                \
+    i32x4 a0[MB_], b0[NB_], a1[MB_], b1[NB_];                                                    \
+    w4::frags<MB_, NB_>(sA0, sB0, 0, r0, c0, lane, a0, b0);                                      \
+    int k = k0;                                                                                  \
+    for (; k + 4 < k1; k += 2) {                                                                 \
+      MOE_I8_STEP(MB_, NB_, sA0, sB0, sA1, sB1, k, true, true, true, RB0, RB1)                   \
+      MOE_I8_STEP(MB_, NB_, sA1, sB1, sA0, sB0, k + 1, true, true, true, RB1, RB0)               \
+    }                                                                                            \
+    if (k + 4 == k1) {                                                                           \
+      if (tail) MOE_I8_MASK(RB0, k + 2);                                                         \
+      MOE_I8_STEP(MB_, NB_, sA0, sB0, sA1, sB1, k, true, true, true, RB0, RB1)                   \
+      if (tail) MOE_I8_MASK(RB1, k + 3);                                                         \
+      MOE_I8_STEP(MB_, NB_, sA1, sB1, sA0, sB0, k + 1, false, true, true, RB1, RB0)              \
+      k += 2;                                                                                    \
+    }                                                                                            \
+    MOE_I8_STEP(MB_, NB_, sA0, sB0, sA1, sB1, k, false, false, true, RB0, RB1)                   \
+    MOE_I8_STEP(MB_, NB_, sA1, sB1, sA0, sB0, k + 1, false, false, false, RB1, RB0)              \
+    bool store = true;                                                                           \
+    if (SPLIT && w.piece >= 0) {                                                                 \
+      /* K piece: publish it; the last piece to arrive sums all of them */                       \
+      i8::store_partial(g.part + (size_t)w.slot * kPartStride, acc, tid);                        \
+      store = split_arrive(&g.split_cnt[w.first], w.S, s_slot);                                  \
+      if (store) {                                                                               \
+        _Pragma("unroll") for (int mb = 0; mb < (MB_); ++mb)                                     \
+          _Pragma("unroll") for (int nb = 0; nb < (NB_); ++nb)                                   \
+            _Pragma("unroll") for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0;                   \
+        for (int pc = 0; pc < w.S; ++pc)                                                         \
+          i8::add_partial(g.part + (size_t)(w.first + pc) * kPartStride, acc, tid);              \
+      }                                                                                          \
+    }                                                                                            \
+    if (store) i8::epilogue<MB_, NB_, GLU, OUTF32>(g, ti, acc, s_xs, r0, c0, lane);              \
+  }
+
+}  // namespace moe

@@ -20,8 +20,10 @@ namespace moe {
 //   hist     [perm_blocks][E] int32 per-block expert histogram
 //   base     [perm_blocks][E] int32 per-block starting rank inside each expert
 //   tiles    [2][257] int32 m-tile prefix sums of the grouped GEMMs
-//   h        [max_rows][max_I] SwiGLU output (fp32 / bf16 / e4m3 codes)
-//   hscale   [max_I/128][rows] fp32 (fp8 layer) / E8M0 words (MX layer): h's scales, K-major
+//   h        [max_rows][max_I] SwiGLU output (fp32 for fp32 and int8 layers / bf16 / e4m3 codes)
+//   hscale   [max_I/128][rows] fp32 (fp8 layer) / E8M0 words (MX layer): h's scales, K-major;
+//            [rows] fp32 (int8 layer)
+//   hq       [max_rows][max_I] int8 codes of h (int8 layer)
 //   xscale   [H/128][rows] fp32 (fp8 layer) / E8M0 words (MX layer, gathered Linear-1 only): the
 //            activation scales of Linear-1's rows, K-major in grouped row order
 //   the single-launch decode layer's regions (bf16 and MX layers with T*K <= kSmallPermPairs, else
@@ -35,7 +37,7 @@ namespace moe {
 //   dflags   kDecodeFlagBytes: the flags many workgroups poll, in copies 4 KiB apart
 //   dcnt     [T][ceil(H/256)] int32 arrival counters of the combine in the Linear-2 epilogue
 struct WsLayout {
-  size_t err = 0, logits = 0, wrt = 0, hist = 0, base = 0, tiles = 0, part = 0, h = 0, hscale = 0, xscale = 0,
+  size_t err = 0, logits = 0, wrt = 0, hist = 0, base = 0, tiles = 0, part = 0, h = 0, hscale = 0, xscale = 0, hq = 0,
          dctrl = 0, dlogits = 0, dhsh = 0, dhshs = 0, dxq = 0, dxqs = 0, dflags = 0, dcnt = 0, total = 0;
   int route_splits = 1;
   int perm_blocks = 0;
@@ -44,6 +46,8 @@ struct WsLayout {
 constexpr int kPermBlock = 256;   // pairs per block in the permutation kernels
 constexpr int kSmallPermPairs = 4096;  // up to this many pairs: one-workgroup permutation
 constexpr int kMaxExperts = 256;
+constexpr int kMaxRowCols = 32768;  // channels of a row that k_rmsnorm and k_quantize_int8 hold in registers
+constexpr int kMaxInt8K = 131071;   // |sum of K products of int8 codes| <= K * 2^14 stays below 2^31
 constexpr int kTileMetaInts = 2048;  // tile metadata of the expert GEMMs (prefix, queues, counters)
 // moe_permute_noalloc: its scratch (error word + per-block histogram and bases) in a static device
 // array of this many bytes; the histogram and bases take 2 * ceil(P / 256) * E * 4 of them.
@@ -54,6 +58,7 @@ constexpr size_t kDecodeFlagBytes = 64 * 4096;  // its polled flags (64 copies, 
 // Validation; returns MOE_OK or the failure status with a reason in *why.
 moe_status check_routing(const moe_config* c, std::string* why);
 moe_status check_config(const moe_config* c, std::string* why);
+moe_status check_norm(const moe_norm_config* c, std::string* why);
 // H, I and I_shared (and the inter of an expert call) must be multiples of this.
 int channel_multiple(int dtype);
 // Workspace layout of a valid config.
@@ -123,6 +128,40 @@ hipError_t launch_quantize_fp8(int rows, int cols, const void* in, uint8_t* code
                                hipStream_t s);
 hipError_t launch_quantize_mx(int rows, int cols, const void* in, uint8_t* codes, uint8_t* scales,
                               hipStream_t s);
+// norm, int8 rows
+struct NormArgs {
+  const void* x = nullptr;
+  const void* g = nullptr;
+  const void* r = nullptr;
+  void* r_out = nullptr;
+  void* y = nullptr;
+  void* codes = nullptr;
+  void* scales = nullptr;
+  int64_t x_bytes = 0, r_bytes = 0, ro_bytes = 0, y_bytes = 0;  // between rows
+  int rows = 0, cols = 0;
+  float eps = 0.f;
+  bool x_f32 = false, r_f32 = false, y_f32 = false, g_f32 = false;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, int quant, hipStream_t s);
+// Rows of `in` (fp32 or bf16, `nsrc` rows) to int8 codes and one scale per row; row i reads source
+// row i, or index[i] / div. name: the launch's profile entry.
+hipError_t launch_quantize_int8(const char* name, const void* in, bool f32, int rows, int nsrc, const int32_t* index, int div,
+                                int cols, void* codes, float* scales, hipStream_t s);
+// int8 grouped product (kernels_gemm_i8.hip)
+struct Int8GemmArgs {
+  int n_exp = 0, n_rows = 0, N = 0, K = 0;
+  const int32_t* offsets = nullptr;  // nullptr: one expert with every row
+  const void* x = nullptr;
+  const float* x_scale = nullptr;
+  const void* w = nullptr;
+  const float* w_scale = nullptr;
+  void* y = nullptr;
+  bool y_f32 = false;
+  int32_t* tiles = nullptr;  // workspace, kTileMetaInts
+  float* part = nullptr;     // workspace, kInt8PartBytes
+};
+constexpr size_t kInt8PartBytes = (size_t)256 * 256 * 256 * 4;  // partial tiles of K-split tiles
+hipError_t launch_int8_gemm(const Int8GemmArgs& a, hipStream_t s);
 // expert FFN
 struct FfnArgs {
   int dtype = MOE_BF16;
@@ -138,12 +177,14 @@ struct FfnArgs {
   const void* w2_scale = nullptr;
   void* y = nullptr;
   void* h = nullptr;          // workspace
-  void* h_scale = nullptr;    // workspace (fp8, MX)
+  void* h_scale = nullptr;    // workspace (fp8, MX, int8)
+  void* h_codes = nullptr;    // workspace (int8)
   void* x_scale_grouped = nullptr;  // workspace (MX): x_scale gathered into grouped row order
   int32_t* tiles = nullptr;   // workspace, kTileMetaInts
   float* part = nullptr;      // workspace, partial tiles of K-split GEMM tiles
 };
 hipError_t launch_expert_ffn(const FfnArgs& a, hipStream_t s);
+hipError_t launch_expert_ffn_int8(const FfnArgs& a, hipStream_t s);
 // single-launch decode layer
 struct DecodeCall {
   moe_config c;

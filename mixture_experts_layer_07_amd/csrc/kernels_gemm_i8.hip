@@ -1,0 +1,289 @@
+// int8 grouped products with a scale per token and per output channel: kernels and launchers (the
+// tile pipeline is in gemm_i8_tile.h).
+//
+//   y[i][n] = (sum_k x[i][k] w[e(i)][n][k]) * x_scale[i] * w_scale[e(i)][n]
+//
+// and, from it, the int8 SwiGLU experts: Linear-1 (gate and up in one product, SiLU(gate) * up kept
+// in fp32), the per-row requantisation, Linear-2. Tile list, ranges and K pieces as for the other
+// types (gemm_common.h).
+#include "gemm_i8_tile.h"
+
+namespace moe {
+
+// Tile prefix sums, cleared counters and a copy of the group offsets that is safe to follow: every
+// offset inside [0, n_rows]. No tile then reads or writes a row outside the buffers, whatever
+// `offsets` holds. offsets == nullptr: one expert with every row.
+constexpr int kI8OffsetsAt = 1536;
+static_assert(kSplitCntOffset + 2 * kMaxSplitItems <= kI8OffsetsAt && kI8OffsetsAt + kMaxExperts + 1 <= kTileMetaInts,
+              "tile metadata region too small");
+__global__ __launch_bounds__(256) void k_build_tiles_i8(const int32_t* __restrict__ offsets, int n_exp, int n_rows, int BM,
+                                                        int32_t* __restrict__ tp) {
+  __shared__ int sbuf[4];
+  const int tid = threadIdx.x;
+  int c = 0;
+  if (tid < n_exp) {
+    const int lo = offsets ? min(max(offsets[tid], 0), n_rows) : 0;
+    const int hi = offsets ? min(max(offsets[tid + 1], 0), n_rows) : n_rows;
+    c = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    tp[kI8OffsetsAt + tid] = lo;
+    if (tid == n_exp - 1) tp[kI8OffsetsAt + n_exp] = hi;
+  }
+  int tot;
+  const int ex = block_exscan_256(c, sbuf, &tot);
+  if (tid < n_exp) tp[tid] = ex;
+  if (tid == 0) tp[n_exp] = tot;
+  for (int i = tid; i < 2 * kQueues + 2 * kMaxSplitItems; i += 256) tp[kTileQueueOffset + i] = 0;
+}
+
+// Largest K offset (a multiple of 128) at which this lane's 16-byte chunk `ch` lies inside a row of
+// K bytes; in rows that end before the chunk's place, the offset that reads the row's first chunk.
+__device__ __forceinline__ int lane_kmax(int K, int ch) {
+  const int last = K - 16 - ch;
+  return last >= 0 ? (last & ~127) : -ch;
+}
+
+// ============================================================================ 256 x 256 tiles
+// Four waves of 128 x 128 (one per SIMD), shorter layouts for ragged m-tiles, as k_gemm_bf16_w4.
+template <bool GLU, bool OUTF32>
+__global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
+  constexpr int BM = 256, BN = 256;
+  __shared__ u32x4 sA0[w4::kStageA];
+  __shared__ u32x4 sA1[w4::kStageA];
+  __shared__ u32x4 sB0[w4::kStageB];
+  __shared__ u32x4 sB1[w4::kStageB];
+  __shared__ float s_xs[BM];
+  __shared__ int tp[kMaxExperts + 1];
+  __shared__ int s_slot[1 + kQueues];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = tid; i <= g.n_exp; i += 256) tp[i] = g.tp[i];
+  __syncthreads();
+  const int total = tp[g.n_exp] * g.n_tiles_n;
+  const int KT = 2 * ((g.K + 255) / 256);  // (an even number of steps)
+  const int kfull = g.K / 128;
+  constexpr size_t kPartStride = kPartFloats;
+
+  const SplitQueue sq = own_plan(total, KT, 16, 256);
+  bool own = true;
+  for (WorkItem w = next_item(g, sq, total, KT, 16, 256, s_slot, own); w.tile >= 0;
+       w = next_item(g, sq, total, KT, 16, 256, s_slot, own)) {
+    const int lane = opaque_tid() & 63;  // (lane-derived offsets are formed per tile)
+    TileInfo ti = decode_tile(w.tile, tp, g, BM);
+    ti.e = __builtin_amdgcn_readfirstlane(ti.e);
+    ti.nt = __builtin_amdgcn_readfirstlane(ti.nt);
+    ti.row0 = __builtin_amdgcn_readfirstlane(ti.row0);
+    ti.mvalid = __builtin_amdgcn_readfirstlane(ti.mvalid);
+    const int k0 = __builtin_amdgcn_readfirstlane(w.k0), k1 = __builtin_amdgcn_readfirstlane(w.k1);
+    const bool tail = k1 > kfull;
+    const int arows = (ti.mvalid + 7) & ~7;  // A rows fetched (8 rows per load instruction)
+    const uint8_t* Ab = a_base(g, ti);
+    const uint8_t* Be = g.B + (size_t)ti.e * g.b_exp;
+    uint32_t oa[8], ob[8];
+    int la_off[8];
+    // (the swizzle gives a lane the same chunk in all its rows: they are 32 apart)
+    const int ch = dma_chunk(wave * 8 + (lane >> 3), lane) * 16;
+    const int kmax = lane_kmax(g.K, ch);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = (j * 4 + wave) * 8 + (lane >> 3);
+      const bool live = (j * 4 + wave) * 8 < arows;  // wave-uniform
+      const int rr = live ? a_row(g, ti, r < ti.mvalid ? r : ti.mvalid - 1) : 0;
+      oa[j] = (uint32_t)rr * (uint32_t)g.lda + (uint32_t)ch;
+      la_off[j] = live ? (j * 4 + wave) * 64 : w4::kSink;
+      ob[j] = (uint32_t)weight_row<GLU, BN>(r, ti.nt, g) * (uint32_t)g.ldb + (uint32_t)ch;
+    }
+    const int bw_off = wave * 64 + lane;
+    if (arows < BM) {  // zero the A rows that are not fetched, in both stages
+      const u32x4 z = {0u, 0u, 0u, 0u};
+      for (int i = arows * 8 + tid; i < BM * 8; i += 256) {
+        sA0[i] = z;
+        sA1[i] = z;
+      }
+    }
+    // the rows' token scales, for the epilogue (read after the K loop's barriers)
+    if (tid < ti.mvalid) s_xs[tid] = g.a_scale[g.a_rows ? a_row(g, ti, tid) : ti.row0 + tid];
+    // K pieces always take the 2 x 2 layout (their partial tiles share one shape)
+    if (w.piece >= 0 || ti.mvalid > 128) {
+      MOE_I8_TILE(4, 4, (wave >> 1) * 128, (wave & 1) * 128, true)
+    } else if (ti.mvalid > 64) {
+      MOE_I8_TILE(4, 2, 0, wave * 64, false)
+    } else if (ti.mvalid > 32) {
+      MOE_I8_TILE(2, 2, 0, wave * 64, false)
+    } else {
+      MOE_I8_TILE(1, 2, 0, wave * 64, false)
+    }
+  }
+}
+
+// ============================================================================ 32 x 256 tiles
+// Decode-sized row groups: 1 x 4 waves of 32 x 64, two workgroups per CU, as k_gemm_bf16_m32.
+template <bool GLU, bool OUTF32>
+__global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
+  constexpr int BM = 32, BN = 256;
+  __shared__ u32x4 sA0[m32::kStageA];
+  __shared__ u32x4 sA1[m32::kStageA];
+  __shared__ u32x4 sB0[w4::kStageB];
+  __shared__ u32x4 sB1[w4::kStageB];
+  __shared__ float s_xs[BM];
+  __shared__ int tp[kMaxExperts + 1];
+  __shared__ int s_slot[1 + kQueues];
+  for (int i = threadIdx.x; i <= g.n_exp; i += 256) tp[i] = g.tp[i];
+  __syncthreads();
+  const int total = tp[g.n_exp] * g.n_tiles_n;
+  const int KT = 2 * ((g.K + 255) / 256);
+  const int kfull = g.K / 128;
+  constexpr size_t kPartStride = 32 * 256;  // words per partial tile
+  const SplitQueue sq = own_plan(total, KT, 16, 512);
+  bool own = true;
+  for (WorkItem w = next_item(g, sq, total, KT, 16, 512, s_slot, own); w.tile >= 0;
+       w = next_item(g, sq, total, KT, 16, 512, s_slot, own)) {
+    const int tid = opaque_tid(), lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    TileInfo ti = decode_tile(w.tile, tp, g, BM);
+    ti.e = __builtin_amdgcn_readfirstlane(ti.e);
+    ti.nt = __builtin_amdgcn_readfirstlane(ti.nt);
+    ti.row0 = __builtin_amdgcn_readfirstlane(ti.row0);
+    ti.mvalid = __builtin_amdgcn_readfirstlane(ti.mvalid);
+    const int k0 = __builtin_amdgcn_readfirstlane(w.k0), k1 = __builtin_amdgcn_readfirstlane(w.k1);
+    const bool tail = k1 > kfull;
+    const int arows = (ti.mvalid + 7) & ~7;
+    const uint8_t* Ab = a_base(g, ti);
+    const uint8_t* Be = g.B + (size_t)ti.e * g.b_exp;
+    uint32_t oa[1], ob[8];
+    int la_off[1];
+    const int ch = dma_chunk(wave * 8 + (lane >> 3), lane) * 16;
+    const int kmax = lane_kmax(g.K, ch);
+    {
+      const int r = wave * 8 + (lane >> 3);
+      const bool live = wave * 8 < arows;  // wave-uniform
+      const int rr = live ? a_row(g, ti, r < ti.mvalid ? r : ti.mvalid - 1) : 0;
+      oa[0] = (uint32_t)rr * (uint32_t)g.lda + (uint32_t)ch;
+      la_off[0] = live ? wave * 64 : m32::kSink;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = (j * 4 + wave) * 8 + (lane >> 3);
+      ob[j] = (uint32_t)weight_row<GLU, BN>(r, ti.nt, g) * (uint32_t)g.ldb + (uint32_t)ch;
+    }
+    const int bw_off = wave * 64 + lane;
+    if (arows < BM) {
+      const u32x4 z = {0u, 0u, 0u, 0u};
+      for (int i = arows * 8 + tid; i < BM * 8; i += 256) {
+        sA0[i] = z;
+        sA1[i] = z;
+      }
+    }
+    if (tid < ti.mvalid) s_xs[tid] = g.a_scale[g.a_rows ? a_row(g, ti, tid) : ti.row0 + tid];
+    MOE_I8_TILE(1, 2, 0, wave * 64, true)
+  }
+}
+
+static int round8(int v) { return ((v + 7) / 8) * 8; }
+
+template <class K>
+static hipError_t launch_one(const char* name, K kernel, int grid, const GemmArgs& g, hipStream_t s) {
+  return timed_launch(name, s, [&] { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, g); });
+}
+
+static hipError_t build_tiles_i8(const int32_t* offsets, int n_exp, int n_rows, int BM, int32_t* tp, hipStream_t s) {
+  return timed_launch("build_tiles_i8", s, [&] {
+    hipLaunchKernelGGL(k_build_tiles_i8, dim3(1), dim3(256), 0, s, offsets, n_exp, n_rows, BM, tp);
+  });
+}
+
+// 256-row tiles when groups average at least 128 rows and the launch has a tile for every CU, 32-row
+// tiles otherwise (the rule of the bf16 kernels, whose pipeline this is).
+static bool large_tiles(int n_rows, int n_exp, int n_tiles_n, int cus) {
+  return n_rows / n_exp >= 128 && (long)((n_rows + 255) / 256) * n_tiles_n >= cus;
+}
+
+static GemmArgs common_args(int32_t* tiles, float* part, int n_exp) {
+  GemmArgs g = GemmArgs{};
+  g.offsets = tiles + kI8OffsetsAt;
+  g.tp = tiles;
+  g.queue = tiles + kTileQueueOffset;
+  g.split_cnt = tiles + kSplitCntOffset;
+  g.part = part;
+  g.n_exp = n_exp;
+  g.a_div = g.a_limit = 1;
+  return g;
+}
+
+hipError_t launch_int8_gemm(const Int8GemmArgs& a, hipStream_t s) {
+  const int cus = dev_info().cus;
+  GemmArgs g = common_args(a.tiles, a.part, a.n_exp);
+  g.A = static_cast<const uint8_t*>(a.x);
+  g.lda = a.K;
+  g.a_scale = a.x_scale;
+  g.B = static_cast<const uint8_t*>(a.w);
+  g.ldb = a.K;
+  g.b_exp = (size_t)a.N * a.K;
+  g.b_scale = a.w_scale;
+  g.b_scale_exp = a.N;
+  g.C = static_cast<uint8_t*>(a.y);
+  g.ldc = (size_t)a.N * (a.y_f32 ? 4 : 2);
+  g.K = a.K;
+  g.N_out = g.Nb = a.N;
+  g.n_tiles_n = (a.N + 255) / 256;
+  const bool large = large_tiles(a.n_rows, a.n_exp, g.n_tiles_n, cus);
+  hipError_t e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s);
+  if (e != hipSuccess) return e;
+  if (large)
+    return a.y_f32 ? launch_one("gemm_i8_f32out", k_gemm_i8_w4<false, true>, round8(cus), g, s)
+                   : launch_one("gemm_i8", k_gemm_i8_w4<false, false>, round8(cus), g, s);
+  return a.y_f32 ? launch_one("gemm_i8_f32out_m32", k_gemm_i8_m32<false, true>, round8(cus * 2), g, s)
+                 : launch_one("gemm_i8_m32", k_gemm_i8_m32<false, false>, round8(cus * 2), g, s);
+}
+
+hipError_t launch_expert_ffn_int8(const FfnArgs& a, hipStream_t s) {
+  const int cus = dev_info().cus, H = a.H, I = a.I;
+  GemmArgs g1 = common_args(a.tiles, a.part, a.n_exp), g2 = g1;
+  // Linear-1: [rows, H] x [2I, H]^T -> h [rows, I] fp32, rows gathered or in place
+  g1.A = static_cast<const uint8_t*>(a.x);
+  g1.lda = H;
+  g1.a_scale = static_cast<const float*>(a.x_scale);
+  g1.a_rows = a.x_rows_index;
+  g1.a_div = a.x_rows_div;
+  g1.a_limit = a.x_rows_limit;
+  g1.B = static_cast<const uint8_t*>(a.w13);
+  g1.ldb = H;
+  g1.b_exp = (size_t)2 * I * H;
+  g1.b_scale = static_cast<const float*>(a.w13_scale);
+  g1.b_scale_exp = (size_t)2 * I;
+  g1.C = static_cast<uint8_t*>(a.h);
+  g1.ldc = (size_t)I * 4;
+  g1.K = H;
+  g1.N_out = g1.glu_I = I;
+  g1.Nb = 2 * I;
+  g1.n_tiles_n = I / 128;
+  // Linear-2: [rows, I] x [H, I]^T -> y [rows, H]
+  g2.queue += kQueues;
+  g2.split_cnt += kMaxSplitItems;
+  g2.A = static_cast<const uint8_t*>(a.h_codes);
+  g2.lda = I;
+  g2.a_scale = static_cast<const float*>(a.h_scale);
+  g2.B = static_cast<const uint8_t*>(a.w2);
+  g2.ldb = I;
+  g2.b_exp = (size_t)H * I;
+  g2.b_scale = static_cast<const float*>(a.w2_scale);
+  g2.b_scale_exp = H;
+  g2.C = static_cast<uint8_t*>(a.y);
+  g2.ldc = (size_t)H * 2;
+  g2.K = I;
+  g2.N_out = g2.Nb = H;
+  g2.n_tiles_n = (H + 255) / 256;
+  const bool large = large_tiles(a.n_rows, a.n_exp, g1.n_tiles_n, cus);
+  const int grid = round8(large ? cus : cus * 2);
+  hipError_t e;
+  if ((e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s)) != hipSuccess) return e;
+  e = large ? launch_one("gemm_i8_gateup_swiglu", k_gemm_i8_w4<true, true>, grid, g1, s)
+            : launch_one("gemm_i8_gateup_swiglu_m32", k_gemm_i8_m32<true, true>, grid, g1, s);
+  if (e != hipSuccess) return e;
+  if ((e = launch_quantize_int8("requantize_int8", a.h, true, a.n_rows, a.n_rows, nullptr, 1, I, a.h_codes,
+                                static_cast<float*>(a.h_scale), s)) != hipSuccess)
+    return e;
+  return large ? launch_one("gemm_i8_down", k_gemm_i8_w4<false, false>, grid, g2, s)
+               : launch_one("gemm_i8_down_m32", k_gemm_i8_m32<false, false>, grid, g2, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,330 @@
+// RMS norm of residual rows with an optional 8-bit output, and the int8 quantisation of rows.
+//
+//   s = x + residual          n[c] = s[c] * g[c] / sqrt(mean(s^2) + eps)
+//   residual_out = round(s)   y = round(n)   codes, scales = the 8-bit form of n
+//
+// One workgroup per row; the row stays in registers between its one read and its writes (thread
+// tid holds the 8-channel groups tid, tid + NT, ..., V of them), so every operand moves once: the
+// kernel is bound by HBM, and for a few rows by its chain of one load, one workgroup reduction and
+// the store. All sums and n itself are fp32; every output is rounded once, from fp32 (the codes
+// from n, not from the rounded y: the int8 experts see no second rounding).
+//
+// The quantiser of the int8 rows needs the row's largest |n|. n is formed as (s g) * rstd, and a
+// product with a positive constant is monotone under rounding, so max |n| = max |s g| * rstd
+// exactly: sum of squares and maximum go through one workgroup reduction.
+#include "device.h"
+#include "internal.h"
+
+namespace moe {
+
+// 8 consecutive channels as fp32. Row strides need not keep rows 16-byte aligned: the vector types
+// carry the element's alignment only, and gfx950 takes unaligned global accesses (the compiler
+// emits one 16-byte load either way).
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+
+__device__ __forceinline__ void unpack8(const u32x4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = bf16_to_f32(w[j] & 0xFFFF);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+// Channels [c, c + 8) of a row of `cols` channels; those past the end read as 0.
+__device__ __forceinline__ void load8(const void* row, bool f32, int c, int cols, float (&v)[8]) {
+  if (c + 8 <= cols) {
+    if (f32) {
+      const u32x4_a4* p = reinterpret_cast<const u32x4_a4*>(static_cast<const float*>(row) + c);
+      const u32x4 a = p[0], b = p[1];
+      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(*reinterpret_cast<const u32x4_a2*>(static_cast<const uint16_t*>(row) + c), v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.f;
+    if (c + j < cols)
+      v[j] = f32 ? static_cast<const float*>(row)[c + j] : bf16_to_f32(static_cast<const uint16_t*>(row)[c + j]);
+  }
+}
+
+__device__ __forceinline__ void store8(void* row, bool f32, int c, int cols, const float (&v)[8]) {
+  const u32x4 b = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
+  if (c + 8 <= cols) {
+    if (f32) {
+      u32x4_a4* p = reinterpret_cast<u32x4_a4*>(static_cast<float*>(row) + c);
+      p[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      p[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else {
+      *reinterpret_cast<u32x4_a2*>(static_cast<uint16_t*>(row) + c) = b;
+    }
+    return;
+  }
+  const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (c + j < cols) {
+      if (f32)
+        static_cast<float*>(row)[c + j] = v[j];
+      else
+        static_cast<uint16_t*>(row)[c + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+// Sum / maximum over a wave, the result in every lane: quad exchanges, rotations inside each row
+// of 16 lanes, the other row of the half, then the two halves.
+__device__ __forceinline__ float wave_sum_dpp(float v) {
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  v += dpp_f32<0x124>(v);
+  v += dpp_f32<0x128>(v);
+  v += __uint_as_float((uint32_t)__builtin_amdgcn_ds_swizzle((int)__float_as_uint(v), 0x401F));
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 0)) +
+         __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 32));
+}
+// (as unsigned bit patterns of non-negative floats: a NaN is the largest, so it reaches the scale)
+__device__ __forceinline__ uint32_t wave_max_dpp(uint32_t m) {
+  m = max(m, dpp_u32<0xB1>(m));
+  m = max(m, dpp_u32<0x4E>(m));
+  m = max_over_quads(m);
+  return max((uint32_t)__builtin_amdgcn_readlane((int)m, 0), (uint32_t)__builtin_amdgcn_readlane((int)m, 32));
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// e4m3 codes of four values within +-448 (clamped here).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  a = __builtin_amdgcn_fmed3f(a, -448.f, 448.f);
+  b = __builtin_amdgcn_fmed3f(b, -448.f, 448.f);
+  c = __builtin_amdgcn_fmed3f(c, -448.f, 448.f);
+  d = __builtin_amdgcn_fmed3f(d, -448.f, 448.f);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
+}
+
+// int8 code of v at a row's scale, as the low byte: round to nearest even of the IEEE quotient,
+// within +-127.
+__device__ __forceinline__ uint32_t int8_code(float v, float scale) {
+  return (uint32_t)(int)__builtin_amdgcn_fmed3f(rintf(v / scale), -127.f, 127.f) & 0xFFu;
+}
+__device__ __forceinline__ void int8_store8(int8_t* row, int c, const float (&v)[8], float scale) {
+  uint32_t w[2] = {0u, 0u};
+  // An all-zero row has scale 0 and codes 0. A row with a NaN or an infinity has a NaN or infinite
+  // scale and codes 0, so that every product with it is NaN.
+  if (scale > 0.f && scale < __builtin_huge_valf()) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j >> 2] |= int8_code(v[j], scale) << (8 * (j & 3));
+  }
+  *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
+}
+
+// Row reduction over the workgroup: every thread gets the sum of `sum` and the maximum of `m`.
+// One barrier; red holds one entry per wave.
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& m, float2* red) {
+  const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  sum = wave_sum_dpp(sum);
+  m = wave_max_dpp(m);
+  if (nw == 1) return;
+  if ((threadIdx.x & 63) == 0) red[wave] = make_float2(sum, __uint_as_float(m));
+  __syncthreads();
+  const int l = threadIdx.x & 15;  // (at most 16 waves: every row of 16 lanes reduces all of them)
+  const float2 r = l < nw ? red[l] : make_float2(0.f, 0.f);
+  sum = r.x;
+  sum += dpp_f32<0xB1>(sum);
+  sum += dpp_f32<0x4E>(sum);
+  sum += dpp_f32<0x124>(sum);
+  sum += dpp_f32<0x128>(sum);
+  m = __float_as_uint(r.y);
+  m = max(m, dpp_u32<0xB1>(m));
+  m = max(m, dpp_u32<0x4E>(m));
+  m = max(m, dpp_u32<0x124>(m));
+  m = max(m, dpp_u32<0x128>(m));
+}
+
+// Q: 0 no codes, else the layer type whose experts read them (MOE_FP8_E4M3, MOE_MXFP4, MOE_INT8).
+// Channels past cols hold zeros (they change neither the sum nor a maximum); cols is a multiple of
+// 128 whenever there are codes, so the 16 lanes of a 128-channel block are all inside or all outside.
+template <int V, int Q>
+__global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
+  __shared__ float2 red[16];
+  const int row = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
+  const bool xf = a.x_f32, rf = a.r_f32;
+  const uint8_t* xr = static_cast<const uint8_t*>(a.x) + (size_t)row * a.x_bytes;
+  float s[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) load8(xr, xf, (v * nt + tid) * 8, a.cols, s[v]);
+  if (a.r) {
+    const uint8_t* rr = static_cast<const uint8_t*>(a.r) + (size_t)row * a.r_bytes;
+    float t[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) load8(rr, rf, (v * nt + tid) * 8, a.cols, t[v]);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[v][j] += t[v][j];
+  }
+  float g[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) load8(a.g, a.g_f32, (v * nt + tid) * 8, a.cols, g[v]);
+  float sum = 0.f;
+  uint32_t m = 0u;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(s[v][j], s[v][j], sum);
+  if (a.r_out) {
+    uint8_t* ro = static_cast<uint8_t*>(a.r_out) + (size_t)row * a.ro_bytes;
+#pragma unroll
+    for (int v = 0; v < V; ++v) store8(ro, rf, (v * nt + tid) * 8, a.cols, s[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[v][j] *= g[v][j];
+      if (Q == MOE_INT8) m = max(m, abs_bits(s[v][j]));
+    }
+  row_reduce(sum, m, red);
+  const float rstd = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[v][j] *= rstd;
+  if (a.y) {
+    uint8_t* yr = static_cast<uint8_t*>(a.y) + (size_t)row * a.y_bytes;
+#pragma unroll
+    for (int v = 0; v < V; ++v) store8(yr, a.y_f32, (v * nt + tid) * 8, a.cols, s[v]);
+  }
+  if (Q == MOE_INT8) {
+    const float scale = __uint_as_float(abs_bits(__uint_as_float(m) * rstd)) / 127.0f;
+    int8_t* cr = static_cast<int8_t*>(a.codes) + (size_t)row * a.cols;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * nt + tid) * 8;
+      if (c < a.cols) int8_store8(cr, c, s[v], scale);
+    }
+    if (tid == 0) static_cast<float*>(a.scales)[row] = scale;
+  } else if (Q != 0) {
+    const int nblk = a.cols / 128;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int grp = v * nt + tid, c = grp * 8, b = grp >> 4;
+      uint32_t bm = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bm = max(bm, abs_bits(s[v][j]));
+      bm = max(bm, dpp_u32<0xB1>(bm));  // the 32 channels of 4 lanes
+      bm = max(bm, dpp_u32<0x4E>(bm));
+      uint32_t lo, hi;
+      if (Q == MOE_FP8_E4M3) {
+        bm = max(bm, dpp_u32<0x124>(bm));  // the 128 channels of 16 lanes
+        bm = max(bm, dpp_u32<0x128>(bm));
+        const float scale = __uint_as_float(bm) / 448.0f;
+        lo = e4m3x4(s[v][0] / scale, s[v][1] / scale, s[v][2] / scale, s[v][3] / scale);
+        hi = e4m3x4(s[v][4] / scale, s[v][5] / scale, s[v][6] / scale, s[v][7] / scale);
+        if (bm == 0u) lo = hi = 0u;
+        if (c < a.cols && (lane & 15) == 0) static_cast<float*>(a.scales)[(size_t)row * nblk + b] = scale;
+      } else {
+        const int ex = (int)(bm >> 23);  // 255 (an infinity or NaN in the block) gives the E8M0 NaN
+        const int code = ex == 255 ? 255 : (ex > 8 ? ex - 8 : 0);
+        const int up = 127 - code;
+        lo = e4m3x4(__builtin_amdgcn_ldexpf(s[v][0], up), __builtin_amdgcn_ldexpf(s[v][1], up),
+                    __builtin_amdgcn_ldexpf(s[v][2], up), __builtin_amdgcn_ldexpf(s[v][3], up));
+        hi = e4m3x4(__builtin_amdgcn_ldexpf(s[v][4], up), __builtin_amdgcn_ldexpf(s[v][5], up),
+                    __builtin_amdgcn_ldexpf(s[v][6], up), __builtin_amdgcn_ldexpf(s[v][7], up));
+        uint32_t word = (uint32_t)code << (8 * ((lane >> 2) & 3));  // the block's four codes in one word
+        word |= dpp_u32<0x124>(word);
+        word |= dpp_u32<0x128>(word);
+        if (c < a.cols && (lane & 15) == 0) static_cast<uint32_t*>(a.scales)[(size_t)b * a.rows + row] = word;
+      }
+      if (c < a.cols)
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.codes) + (size_t)row * a.cols + c) = make_uint2(lo, hi);
+    }
+  }
+}
+
+// Rows to int8, one workgroup per row: scale = absmax / 127, code = rint(v / scale). Destination
+// row i reads source row i, or (index given) row index[i] / div of nsrc, clamped into the source.
+template <int V>
+__global__ __launch_bounds__(1024) void k_quantize_int8(const uint8_t* __restrict__ in, bool f32, int nsrc,
+                                                        const int32_t* __restrict__ index, int div, int cols,
+                                                        int8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ float2 red[16];
+  const int row = blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
+  unsigned src = (unsigned)row;
+  if (index) {
+    src = (unsigned)index[row] / (unsigned)div;
+    if (src >= (unsigned)nsrc) src = 0;  // (slots behind dropped pairs stay unwritten)
+  }
+  const uint8_t* p = in + (size_t)src * cols * (f32 ? 4 : 2);
+  float s[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) load8(p, f32, (v * nt + tid) * 8, cols, s[v]);
+  uint32_t m = 0u;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(s[v][j]));
+  float unused = 0.f;
+  row_reduce(unused, m, red);
+  const float scale = __uint_as_float(m) / 127.0f;
+  int8_t* cr = codes + (size_t)row * cols;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * nt + tid) * 8;
+    if (c < cols) int8_store8(cr, c, s[v], scale);
+  }
+  if (tid == 0) scales[row] = scale;
+}
+
+// Groups per thread and threads of a row of `cols` channels: one group per thread (the shortest
+// chain) while that fits a workgroup, the fewest groups that do otherwise (cols <= kMaxRowCols).
+static void row_shape(int cols, int* V, int* nt) {
+  const int groups = (cols + 7) / 8;
+  int v = 1;
+  while (groups > v * 1024) v *= 2;
+  *V = v;
+  *nt = ((groups + v - 1) / v + 63) / 64 * 64;
+}
+
+template <int Q>
+static hipError_t launch_norm_q(const char* name, const NormArgs& a, hipStream_t s) {
+  int V, nt;
+  row_shape(a.cols, &V, &nt);
+  return timed_launch(name, s, [&] {
+    switch (V) {
+      case 1: hipLaunchKernelGGL((k_rmsnorm<1, Q>), dim3(a.rows), dim3(nt), 0, s, a); break;
+      case 2: hipLaunchKernelGGL((k_rmsnorm<2, Q>), dim3(a.rows), dim3(nt), 0, s, a); break;
+      default: hipLaunchKernelGGL((k_rmsnorm<4, Q>), dim3(a.rows), dim3(nt), 0, s, a);
+    }
+  });
+}
+
+hipError_t launch_rmsnorm(const NormArgs& a, int quant, hipStream_t s) {
+  switch (quant) {
+    case MOE_FP8_E4M3: return launch_norm_q<MOE_FP8_E4M3>("rmsnorm_fp8", a, s);
+    case MOE_MXFP4: return launch_norm_q<MOE_MXFP4>("rmsnorm_mx", a, s);
+    case MOE_INT8: return launch_norm_q<MOE_INT8>("rmsnorm_int8", a, s);
+    default: return launch_norm_q<0>("rmsnorm", a, s);
+  }
+}
+
+hipError_t launch_quantize_int8(const char* name, const void* in, bool f32, int rows, int nsrc, const int32_t* index, int div,
+                                int cols, void* codes, float* scales, hipStream_t s) {
+  int V, nt;
+  row_shape(cols, &V, &nt);
+  const uint8_t* p = static_cast<const uint8_t*>(in);
+  int8_t* c = static_cast<int8_t*>(codes);
+  return timed_launch(name, s, [&] {
+    switch (V) {
+      case 1: hipLaunchKernelGGL(k_quantize_int8<1>, dim3(rows), dim3(nt), 0, s, p, f32, nsrc, index, div, cols, c, scales); break;
+      case 2: hipLaunchKernelGGL(k_quantize_int8<2>, dim3(rows), dim3(nt), 0, s, p, f32, nsrc, index, div, cols, c, scales); break;
+      default: hipLaunchKernelGGL(k_quantize_int8<4>, dim3(rows), dim3(nt), 0, s, p, f32, nsrc, index, div, cols, c, scales);
+    }
+  });
+}
+
+}  // namespace moe

@@ -217,6 +217,9 @@ hipError_t launch_gather(const moe_config& c, const int32_t* sorted_pair, const 
       hipLaunchKernelGGL(k_gather<2>, grid, dim3(256), 0, s, sorted_pair, c.K, P, c.T, xi,
                          (size_t)c.H * 2, xo, x_scale, c.H);
     });
+  if (c.dtype == MOE_INT8)
+    return launch_quantize_int8("gather_quant_int8", x, false, P, c.T, sorted_pair, c.K, c.H, x_perm,
+                                static_cast<float*>(x_scale), s);
   const size_t rb = (size_t)c.H * (c.dtype == MOE_F32 ? 4 : 2);
   return timed_launch("gather", s, [&] {
     hipLaunchKernelGGL(k_gather<0>, grid, dim3(256), 0, s, sorted_pair, c.K, P, c.T, xi, rb, xo,

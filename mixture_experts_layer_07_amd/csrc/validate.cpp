@@ -44,6 +44,25 @@ moe_status check_routing(const moe_config* c, std::string* why) {
   return MOE_OK;
 }
 
+moe_status check_norm(const moe_norm_config* c, std::string* why) {
+  auto bad = [&](moe_status s, const char* msg) {
+    if (why) *why = msg;
+    return s;
+  };
+  if (!c) return bad(MOE_ERR_INVALID_ARG, "config is NULL");
+  if (c->rows < 0 || c->cols < 1) return bad(MOE_ERR_INVALID_ARG, "rows must be >= 0 and cols positive");
+  if (c->cols > kMaxRowCols) return bad(MOE_ERR_UNSUPPORTED, "cols above 32768 is not supported");
+  for (const int t : {c->x_dtype, c->residual_dtype, c->weight_dtype, c->y_dtype})
+    if (t != MOE_F32 && t != MOE_BF16) return bad(MOE_ERR_INVALID_ARG, "x, residual, weight and y are fp32 or bf16");
+  if (c->quant != 0 && c->quant != MOE_FP8_E4M3 && c->quant != MOE_MXFP4 && c->quant != MOE_INT8)
+    return bad(MOE_ERR_INVALID_ARG, "quant must be 0, MOE_FP8_E4M3, MOE_MXFP4 or MOE_INT8");
+  if (c->quant != 0 && c->cols % 128) return bad(MOE_ERR_UNSUPPORTED, "codes need cols a multiple of 128");
+  if (!(c->eps >= 0.f) || c->eps > 3.0e38f) return bad(MOE_ERR_INVALID_ARG, "eps must be finite and not negative");
+  for (const int64_t s : {c->x_stride, c->residual_stride, c->residual_out_stride, c->y_stride})
+    if (s != 0 && s < c->cols) return bad(MOE_ERR_INVALID_ARG, "a row stride must be 0 (contiguous) or at least cols");
+  return MOE_OK;
+}
+
 moe_status check_config(const moe_config* c, std::string* why) {
   auto bad = [&](moe_status s, const char* msg) {
     if (why) *why = msg;
@@ -52,7 +71,8 @@ moe_status check_config(const moe_config* c, std::string* why) {
   const moe_status r = check_routing(c, why);
   if (r != MOE_OK) return r;
   if (c->H < 1 || c->I < 1) return bad(MOE_ERR_INVALID_ARG, "T, H, I, E and K must be positive");
-  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16 && c->dtype != MOE_FP8_E4M3 && c->dtype != MOE_MXFP4)
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16 && c->dtype != MOE_FP8_E4M3 && c->dtype != MOE_MXFP4 &&
+      c->dtype != MOE_INT8)
     return bad(MOE_ERR_INVALID_ARG, "unknown dtype");
   if (c->I_shared < 0) return bad(MOE_ERR_INVALID_ARG, "I_shared must be >= 0");
   if (c->out_dtype != MOE_F32 && c->out_dtype != MOE_BF16)
@@ -64,7 +84,7 @@ moe_status check_config(const moe_config* c, std::string* why) {
     return bad(MOE_ERR_UNSUPPORTED,
                c->dtype == MOE_F32     ? "fp32 layers need H, I, I_shared multiples of 4"
                : c->dtype == MOE_MXFP4 ? "MXFP4 layers need H, I, I_shared multiples of 256"
-                                       : "bf16/fp8 layers need H, I, I_shared multiples of 128");
+                                       : "bf16/fp8/int8 layers need H, I, I_shared multiples of 128");
   const int64_t P = (int64_t)c->T * c->K;
   if (P >= (int64_t(1) << 31)) return bad(MOE_ERR_INVALID_ARG, "T*K must be below 2^31");
   const int64_t maxI = c->I > c->I_shared ? c->I : c->I_shared;
@@ -72,6 +92,8 @@ moe_status check_config(const moe_config* c, std::string* why) {
     return bad(MOE_ERR_UNSUPPORTED, "buffers above 2^40 elements are not supported");
   if ((int64_t)c->H * 2 * maxI >= (int64_t(1) << 31))
     return bad(MOE_ERR_UNSUPPORTED, "one expert above 2^31 elements is not supported");
+  if (c->dtype == MOE_INT8 && (c->H > kMaxRowCols || maxI > kMaxRowCols))
+    return bad(MOE_ERR_UNSUPPORTED, "int8 layers need H, I and I_shared of at most 32768");
   return MOE_OK;
 }
 
@@ -131,16 +153,21 @@ WsLayout layout(const moe_config& c) {
   off = align256(off + (size_t)L.perm_blocks * E * 4);
   L.tiles = off;
   off = align256(off + (size_t)kTileMetaInts * 4);
-  // partial tiles of K-split GEMM tiles: bf16 up to 256 of 256 x 256 fp32 (256-row tiles) or 512
+  // partial tiles of K-split GEMM tiles: bf16 and int8 up to 256 of 256 x 256 fp32 (256-row tiles) or 512
   // of 32 x 256 (32-row tiles), 64 MiB; MX up to 512 of 32 x 256, 16 MiB
   L.part = off;
-  off = align256(off + (c.dtype == MOE_BF16 ? (size_t)256 * 256 * 256 * 4
+  off = align256(off + (c.dtype == MOE_BF16 || c.dtype == MOE_INT8 ? (size_t)256 * 256 * 256 * 4
                                             : (c.dtype == MOE_MXFP4 ? (size_t)512 * 32 * 256 * 4 : 0)));
-  const size_t elem = c.dtype == MOE_F32 ? 4 : (c.dtype == MOE_BF16 ? 2 : 1);
+  const size_t elem = c.dtype == MOE_F32 || c.dtype == MOE_INT8 ? 4 : (c.dtype == MOE_BF16 ? 2 : 1);
   L.h = off;
   off = align256(off + P * maxI * elem);
   L.hscale = off;  // fp8: one fp32 per row per 128 channels; MX: one word of four E8M0 codes
   off = align256(off + (c.dtype == MOE_FP8_E4M3 || c.dtype == MOE_MXFP4 ? P * (maxI / 128) * 4 : 0));
+  if (c.dtype == MOE_INT8) {  // one scale per row of h, and its codes
+    off = align256(off + P * 4);
+    L.hq = off;
+    off = align256(off + P * maxI);
+  }
   L.xscale = off;  // the same for Linear-1's activation rows, K-major in grouped row order
   off = align256(off + (c.dtype == MOE_FP8_E4M3 || c.dtype == MOE_MXFP4 ? P * (H / 128) * 4 : 0));
   const bool dec = decode_supported(c, nullptr);

@@ -20,6 +20,8 @@ Recipe (weights drawn N(0, 1/fan_in), i.e. variance 1/fan_in):
            b + U{-1,0,1} (rms factor 1.32) with b = 127 + round(log2(fan_in^-1/2 / (2.93 * 1.32))),
            so that the weights have about the N(0,1/fan_in) spread of the other layers (119 for
            H = 7168, 120 for I = 2048); scale codes in the library's [in/128][out rows][4] layout.
+  int8     weights drawn in fp32 as above, then per output channel (row) scale = absmax/127 and
+           codes = round-half-even(w / scale).
 Generator seed: (seed << 24) | (tensor_id << 16) | expert.
 x, W_r and the bias are drawn on the CPU (so every machine sees the same
 values); the expert weights are drawn on `device` with one generator per
@@ -98,6 +100,13 @@ def fp8_block_quantise(w):
     return codes, s.contiguous()
 
 
+def int8_row_quantise(w):
+    """fp32 [N,K] -> (int8 codes [N,K], fp32 scales [N]); input preparation."""
+    s = w.abs().amax(dim=1) / 127.0
+    safe = torch.where(s == 0, torch.ones_like(s), s)
+    return (w / safe[:, None]).round().clamp(-127, 127).to(torch.int8), s.contiguous()
+
+
 E2M1_RMS = 2.93 * 1.32  # rms of a uniform e2m1 code times that of 2^j, j uniform in {-1, 0, 1}
 
 
@@ -114,7 +123,7 @@ def mx_weight(rows, cols, seed, tensor, expert, device):
 def expert_weights(cfg: LayerConfig, e, device="cpu", shared=False):
     """(w13 [2I,H], w2 [H,I]) of routed expert e (or the shared expert) in the layer dtype.
 
-    For fp8 and mxfp4 returns (w13_codes, w13_scale, w2_codes, w2_scale).
+    For fp8, mxfp4 and int8 returns (w13_codes, w13_scale, w2_codes, w2_scale).
     """
     I = cfg.I_shared if shared else cfg.I
     t13, t2 = ("w13s", "w2s") if shared else ("w13", "w2")
@@ -128,13 +137,14 @@ def expert_weights(cfg: LayerConfig, e, device="cpu", shared=False):
         return w13, w2
     if cfg.dtype == "bf16":
         return w13.to(torch.bfloat16), w2.to(torch.bfloat16)
-    c13, s13 = fp8_block_quantise(w13)
-    c2, s2 = fp8_block_quantise(w2)
+    quantise = int8_row_quantise if cfg.dtype == "int8" else fp8_block_quantise
+    c13, s13 = quantise(w13)
+    c2, s2 = quantise(w2)
     return c13, s13, c2, s2
 
 
 def make_expert_weights(cfg: LayerConfig, device="cpu", shared=False):
-    """Stacked expert weights on `device`: dict with w13 [n,2I,H], w2 [n,H,I] (+ scales for fp8)."""
+    """Stacked expert weights on `device`: dict with w13 [n,2I,H], w2 [n,H,I] (+ scales for fp8, mxfp4, int8)."""
     n = 1 if shared else cfg.E
     I = cfg.I_shared if shared else cfg.I
     if cfg.dtype == "mxfp4":
@@ -146,11 +156,13 @@ def make_expert_weights(cfg: LayerConfig, device="cpu", shared=False):
         for e in range(n):
             w13[e], s13[e], w2[e], s2[e] = expert_weights(cfg, e, device, shared)
         return {"w13": w13, "w2": w2, "w13_scale": s13, "w2_scale": s2}
-    if cfg.dtype == "fp8":
-        w13 = torch.empty((n, 2 * I, cfg.H), dtype=torch.uint8, device=device)
-        w2 = torch.empty((n, cfg.H, I), dtype=torch.uint8, device=device)
-        s13 = torch.empty((n, 2 * I // 128, cfg.H // 128), dtype=torch.float32, device=device)
-        s2 = torch.empty((n, cfg.H // 128, I // 128), dtype=torch.float32, device=device)
+    if cfg.dtype in ("fp8", "int8"):
+        i8 = cfg.dtype == "int8"
+        ct = torch.int8 if i8 else torch.uint8
+        w13 = torch.empty((n, 2 * I, cfg.H), dtype=ct, device=device)
+        w2 = torch.empty((n, cfg.H, I), dtype=ct, device=device)
+        s13 = torch.empty((n, 2 * I) if i8 else (n, 2 * I // 128, cfg.H // 128), dtype=torch.float32, device=device)
+        s2 = torch.empty((n, cfg.H) if i8 else (n, cfg.H // 128, I // 128), dtype=torch.float32, device=device)
         for e in range(n):
             c13, a13, c2, a2 = expert_weights(cfg, e, device, shared)
             w13[e], s13[e], w2[e], s2[e] = c13, a13, c2, a2

@@ -4,8 +4,11 @@ route -> permute -> expert FFN (routed experts, then the shared expert if any) -
 With fused=True (bf16 and MX layers with T*K <= 4096) the whole layer is one call, moe_layer_decode: one
 kernel launch that fills the same buffers (it reads the router weights K-major, transposed once
 at construction).
-With gather=True (the default) the permute stage only builds the pair order (and, for fp8 and
-MX layers, quantises the T input rows once) and Linear-1 of the routed experts reads the token rows in
+With norm_weight given, forward(x, residual) first runs moe_rmsnorm on x + residual (the residual is
+updated in place): its rows feed the router and, quantised in the same pass, the experts of fp8, MX
+and int8 layers.
+With gather=True (the default) the permute stage only builds the pair order (and, for fp8, MX and
+int8 layers without a norm, quantises the T input rows once) and Linear-1 of the routed experts reads the token rows in
 place (moe_expert_ffn_gather); with gather=False the permute stage also writes the permuted
 copy x_perm that moe_expert_ffn reads. Buffers are allocated once at construction and reused by
 every forward; the calls are enqueued on the current stream and none of them waits.
@@ -27,8 +30,9 @@ from .configs import LayerConfig
 
 class MoELayer:
     def __init__(self, cfg: LayerConfig, w_router, bias, experts, shared=None, device="cuda",
-                 gather=True, fused=False, overlap_shared=True):
-        """experts / shared: dicts with w13, w2 (+ w13_scale, w2_scale for fp8 / mxfp4) on `device`."""
+                 gather=True, fused=False, overlap_shared=True, norm_weight=None, norm_eps=1e-6):
+        """experts / shared: dicts with w13, w2 (+ w13_scale, w2_scale for fp8 / mxfp4 / int8) on `device`.
+        norm_weight: [H] fp32 or bf16, the RMS norm in front of the layer (None: x comes normed)."""
         self.cfg = cfg
         self.gather = gather or fused
         self.fused = fused
@@ -38,7 +42,9 @@ class MoELayer:
         act = torch.float32 if cfg.dtype == "f32" else torch.bfloat16
         self.fp8 = cfg.dtype == "fp8"
         self.mx = cfg.dtype == "mxfp4"
-        self.quant = self.fp8 or self.mx   # experts read e4m3 codes plus scales
+        self.i8 = cfg.dtype == "int8"
+        self.quant = self.fp8 or self.mx or self.i8   # experts read e4m3 or int8 codes plus scales
+        codes = torch.int8 if self.i8 else torch.uint8
         dev = torch.device(device)
         self.w_router = w_router
         # the single launch reads the router weights K-major ([E, H], as the expert weights are
@@ -58,14 +64,17 @@ class MoELayer:
         self.pair_pos = torch.empty(P, **i32)
         self.x_perm = self.x_perm_scale = None
         if not self.gather:
-            self.x_perm = torch.empty((P, H), dtype=torch.uint8 if self.quant else act, device=dev)
+            self.x_perm = torch.empty((P, H), dtype=codes if self.quant else act, device=dev)
             if self.quant:
                 self.x_perm_scale = self._scales(P, H, dev)
         self.xq = self.xq_scale = None
         if self.quant and not fused and (self.gather or self.shared is not None):
-            # the e4m3 codes of the T input rows, read by the gathered Linear-1 and the shared expert
-            self.xq = torch.empty((T, H), dtype=torch.uint8, device=dev)
+            # the codes of the T input rows, read by the gathered Linear-1 and the shared expert
+            self.xq = torch.empty((T, H), dtype=codes, device=dev)
             self.xq_scale = self._scales(T, H, dev)
+        self.norm_weight = norm_weight
+        self.norm_eps = norm_eps
+        self.xn = torch.empty((T, H), dtype=act, device=dev) if norm_weight is not None else None
         # expert outputs: fp32 for the fp32 layer, bf16 otherwise
         ydt = torch.float32 if cfg.dtype == "f32" else torch.bfloat16
         self.y_perm = torch.empty((P, H), dtype=ydt, device=dev)
@@ -86,14 +95,23 @@ class MoELayer:
             self.side = torch.cuda.Stream(device=dev)
 
     def _scales(self, rows, cols, dev):
-        """fp8: [rows, cols/128] fp32; MX: the [cols/128][rows][4] E8M0 code array."""
+        """fp8: [rows, cols/128] fp32; MX: the [cols/128][rows][4] E8M0 code array; int8: [rows] fp32."""
         if self.mx:
             return torch.empty((cols // 128, rows, 4), dtype=torch.uint8, device=dev)
-        return torch.empty((rows, cols // 128), dtype=torch.float32, device=dev)
+        return torch.empty((rows,) if self.i8 else (rows, cols // 128), dtype=torch.float32, device=dev)
 
     def _quantize(self, x):
-        q = B.moe_quantize_mx if self.mx else B.moe_quantize_fp8
+        if self.norm_weight is not None:  # (moe_rmsnorm has written the codes)
+            return
+        q = B.moe_quantize_mx if self.mx else (B.moe_quantize_int8 if self.i8 else B.moe_quantize_fp8)
         q(self.cfg.T, self.cfg.H, x, self.xq, self.xq_scale)
+
+    def norm(self, x, residual=None):
+        """The normed rows of x + residual (residual becomes the sum), with the experts' codes."""
+        q = None if self.xq is None else ("mx" if self.mx else ("int8" if self.i8 else "fp8"))
+        B.moe_rmsnorm(x, self.norm_weight, self.norm_eps, y=self.xn, residual=residual, residual_out=residual,
+                      quant=q, codes=self.xq, scales=self.xq_scale)
+        return self.xn
 
     def route(self, x):
         B.moe_route(self.c, x, self.w_router, self.bias, self.topk_ids, self.topk_weights, self.ws)
@@ -136,7 +154,11 @@ class MoELayer:
     def combine(self):
         B.moe_combine(self.c, self.pair_pos, self.topk_weights, self.y_perm, self.y_shared, self.out)
 
-    def forward(self, x):
+    def forward(self, x, residual=None):
+        if self.norm_weight is not None:
+            x = self.norm(x, residual)
+        elif residual is not None:
+            raise ValueError("a residual needs norm_weight")
         if self.fused:
             ex, sh = self.experts, self.shared
             shg = (lambda k: None) if sh is None else sh.get  # noqa: E731
@@ -154,7 +176,7 @@ class MoELayer:
             self.combine()
             return self.out
         main = torch.cuda.current_stream(x.device)
-        # (fp8 / MX with gathered rows: the shared expert reads the codes the permute stage writes)
+        # (fp8 / MX / int8 with gathered rows: the shared expert reads the codes the permute stage writes)
         early = not (self.quant and self.gather) and self.cfg.P <= 4096
         if not early:
             self.route(x)

@@ -72,6 +72,9 @@ transposed operand fails at least one of them:
     block maximum always in e4m3's top binade, the error bound; the nibble order
     and block orientation of dequantize_weight_mx on hand-built bytes; an MX layer
     whose inputs are exactly representable equals the fp64 layer on those values.
+  * quantize_rows_int8 and rmsnorm (tests/test_int8_norm_host.py): representable rows round-trip,
+    ties go to the even code, zero and non-finite rows; the norm of hand-computed rows, unit rms of
+    the output, invariance under scaling.
 No function here is "parity unpinned".
 """
 import math
@@ -86,6 +89,7 @@ __all__ = [
     "quantize_rows_fp8", "dequantize_rows_fp8", "dequantize_weight_blocks",
     "E2M1_MAX", "MX_BLOCK", "e2m1_decode", "e2m1_decode_array", "e8m0_decode", "mx_scale_code",
     "quantize_rows_mx", "dequantize_rows_mx", "unpack_e2m1", "dequantize_weight_mx",
+    "quantize_rows_int8", "dequantize_rows_int8", "rmsnorm",
     "silu", "swiglu_hidden", "swiglu_expert", "expert_ffn", "combine",
     "moe_layer", "dense_mix",
 ]
@@ -450,6 +454,37 @@ def dequantize_weight_mx(packed, scale_codes, block=MX_BLOCK):
     vals = e2m1_decode_array(unpack_e2m1(packed))
     N, K = vals.shape
     return (vals.reshape(N, K // block, block) * e8m0_decode(scale_codes)[..., None]).reshape(N, K)
+
+
+# ----------------------------------------------------------------------------- int8, norm
+
+def quantize_rows_int8(a):
+    """int8 quantisation of rows in fp32 (the precision the kernels quantise in).
+
+    a [R,C] -> (codes [R,C] int8, scales [R] fp32): scale = absmax / 127, code = a / scale rounded
+    to nearest even. An all-zero row has scale 0 and codes 0; a row with a NaN or an infinity has
+    that scale and codes 0.
+    """
+    a32 = np.asarray(a, np.float32)
+    scale = (np.abs(a32).max(axis=1) / np.float32(127)).astype(np.float32)
+    live = np.isfinite(scale) & (scale > 0)
+    safe = np.where(live, scale, np.float32(1)).astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        q = np.clip(np.rint((a32 / safe[:, None]).astype(np.float32)), -127, 127)
+    return np.where(live[:, None], q, 0).astype(np.int8), scale
+
+
+def dequantize_rows_int8(codes, scales):
+    """Inverse of quantize_rows_int8 in fp64 (also for weight rows: one scale per row)."""
+    return np.asarray(codes, np.float64) * np.asarray(scales, np.float64)[:, None]
+
+
+def rmsnorm(x, weight, eps, residual=None):
+    """s = x + residual, n = s * weight / sqrt(mean(s^2) + eps) per row, in fp64: (n, s)."""
+    s = np.asarray(x, np.float64)
+    if residual is not None:
+        s = s + np.asarray(residual, np.float64)
+    return s / np.sqrt((s * s).mean(axis=1, keepdims=True) + eps) * np.asarray(weight, np.float64), s
 
 
 # ----------------------------------------------------------------------------- experts

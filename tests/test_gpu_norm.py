@@ -1,0 +1,259 @@
+"""moe_rmsnorm and moe_quantize_int8 (through the C ABI) against the fp64 oracle.
+
+Tolerances. In fp32, with u = 2^-24 the largest relative rounding: s = x + r is one rounding; the
+sum of squares has non-negative terms, at most 32 in a row per thread and 12 levels of pairwise sums
+above, so its relative error is at most (32 + 12 + 2) u, with s counted twice; the square root
+halves that, the mean, the addition of eps, the root and the quotient add at most 4 u; n adds two
+products and the rounding of s: 23 + 4 + 3 = 30 u, below 2^-19. Stored values add half a step of
+their type (bf16 2^-8, e4m3 2^-4 of the value, below e4m3's normals 2^-10 of the scale, int8 half a scale).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from mixture_experts_layer_07_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+TY = {"bf16": torch.bfloat16, "f32": torch.float32}
+N_TOL = 2.0 ** -19
+HALF = {"bf16": 2.0 ** -8, "f32": 0.0}
+
+
+def make(rows, cols, ty, pad, seed, spread=1.0):
+    """A [rows, cols] device tensor with row stride cols + pad, and NaN around the rows."""
+    g = torch.Generator().manual_seed(seed)
+    t = torch.full((rows, cols + pad), float("nan"))
+    t[:, :cols] = torch.randn((rows, cols), generator=g) * spread
+    return t.to(TY[ty]).cuda()[:, :cols]
+
+
+def guarded(rows, cols, ty, pad):
+    t = torch.full((rows + 1, cols + pad), -7.0, dtype=TY[ty], device="cuda")
+    return t, t[:rows, :cols]
+
+
+def codes_for(quant, rows, cols):
+    ct = torch.int8 if quant == "int8" else torch.uint8
+    shape, st = {"fp8": ((rows, cols // 128), torch.float32), "mx": ((cols // 128, rows, 4), torch.uint8),
+                 "int8": ((rows,), torch.float32)}[quant]
+    c = torch.full((rows + 1, cols), 99, dtype=ct, device="cuda")
+    return c, torch.full(shape, 99, dtype=st, device="cuda")
+
+
+def mx_codes(scales):
+    s = scales.cpu().numpy()
+    return np.ascontiguousarray(s.transpose(1, 0, 2)).reshape(s.shape[1], -1)
+
+
+def check_codes(quant, n32, codes, scales):
+    """Codes and scales are those of the fp32 rows n32, bit for bit."""
+    c = codes.cpu().numpy()
+    if quant == "int8":
+        want, s = orc.quantize_rows_int8(n32)
+        got_s = scales.cpu().numpy()
+    elif quant == "fp8":
+        want, s = orc.quantize_rows_fp8(n32)
+        got_s = scales.cpu().numpy()
+    else:
+        want, s = orc.quantize_rows_mx(n32)
+        got_s = mx_codes(scales)
+    assert (got_s == s).all(), f"{int((got_s != s).sum())} scales differ"
+    assert (c == want).all(), f"{int((c != want).sum())} codes differ"
+
+
+def check_values(quant, ref, codes, scales):
+    """The values that the codes stand for, against n in 64 bits."""
+    c = codes.cpu().numpy()
+    if quant == "int8":
+        s = np.repeat(scales.cpu().numpy().astype(np.float64)[:, None], ref.shape[1], 1)
+        v, half = c.astype(np.float64) * s, 0.5 * s
+    elif quant == "fp8":
+        s = np.repeat(scales.cpu().numpy().astype(np.float64), 128, 1)
+        v, half = orc.e4m3_decode_array(c) * s, np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * s)
+    else:
+        s = np.repeat(orc.e8m0_decode(mx_codes(scales)), 32, 1)
+        v = orc.e4m3_decode_array(c) * s
+        # the scaled maximum lies in [256, 512): above 448 it saturates, by at most 512 - 448
+        half = np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10 * s)
+        half = np.where(np.abs(ref) > 448 * s, np.abs(ref) - 448 * s, half)
+    assert (np.abs(v - ref) <= half * (1 + 2.0 ** -17) + 2.0 ** -17 * np.abs(ref)).all()
+
+
+# rows, cols, x, residual, y, weight, quant, pad
+CASES = [
+    (1, 7168, "bf16", "bf16", "bf16", "bf16", "fp8", 0),
+    (128, 7168, "f32", "bf16", "bf16", "bf16", "int8", 0),
+    (5, 1, "bf16", "bf16", "bf16", "bf16", None, 0),
+    (3, 7, "f32", "f32", "f32", "f32", None, 1),
+    (17, 9, "bf16", None, "f32", "f32", None, 3),
+    (33, 511, "bf16", "f32", "f32", "bf16", None, 1),
+    (33, 4099, "bf16", "bf16", "bf16", "bf16", None, 2),
+    (9, 8192, "bf16", "bf16", "f32", "f32", "mx", 0),
+    (7, 8320, "f32", "f32", "f32", "bf16", "int8", 2),
+    (7, 8320, "bf16", "bf16", "bf16", "f32", "fp8", 2),
+    (4, 16384 + 128, "bf16", "f32", "f32", "bf16", "mx", 64),
+    (3, 32768, "f32", "bf16", "f32", "bf16", "int8", 0),
+    (3, 32767, "bf16", "bf16", "f32", "bf16", None, 0),
+    (2, 128, "bf16", "bf16", "f32", "bf16", "mx", 0),
+    (2, 128, "bf16", "bf16", "f32", "bf16", "fp8", 5),
+    (300, 256, "bf16", None, "f32", "bf16", "int8", 0),
+    (1027, 384, "bf16", "bf16", "bf16", "bf16", "int8", 0),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_rmsnorm(case):
+    rows, cols, xt, rt, yt, wt, quant, pad = case
+    print("rmsnorm", case, flush=True)
+    x = make(rows, cols, xt, pad, 1)
+    r = make(rows, cols, rt, pad, 2, 3.0) if rt else None
+    g = make(1, cols, wt, 0, 3, 0.3)[0] + 1
+    ybuf, y = guarded(rows, cols, yt, pad)
+    rbuf, ro = guarded(rows, cols, rt, pad) if rt else (None, None)
+    cbuf, sc = codes_for(quant, rows, cols) if quant else (None, None)
+    B.moe_rmsnorm(x, g, 1e-5, y=y, residual=r, residual_out=ro, quant=quant, codes=cbuf[:rows] if quant else None, scales=sc)
+    torch.cuda.synchronize()
+    n, s = orc.rmsnorm(x.double().cpu().numpy(), g.double().cpu().numpy(), 1e-5, None if r is None else r.double().cpu().numpy())
+    got = y.double().cpu().numpy()
+    assert (np.abs(got - n) <= (N_TOL + HALF[yt]) * (1 + 2.0 ** -16) * np.abs(n)).all()
+    assert (ybuf[rows] == -7).all() and (ybuf[:, cols:] == -7).all(), "wrote outside y"
+    if rt:
+        assert (np.abs(ro.double().cpu().numpy() - s) <= (2.0 ** -24 + HALF[rt]) * (1 + 2.0 ** -16) * np.abs(s)).all()
+        assert (rbuf[rows] == -7).all() and (rbuf[:, cols:] == -7).all(), "wrote outside residual_out"
+    if quant:
+        assert (cbuf[rows] == 99).all(), "wrote outside codes"
+        check_values(quant, n, cbuf[:rows], sc)
+        if yt == "f32":
+            check_codes(quant, y.cpu().numpy(), cbuf[:rows], sc)
+        # codes alone are the same codes
+        c2, s2 = codes_for(quant, rows, cols)
+        B.moe_rmsnorm(x, g, 1e-5, residual=r, quant=quant, codes=c2[:rows], scales=s2)
+        assert torch.equal(c2, cbuf) and torch.equal(s2, sc)
+
+
+@pytest.mark.parametrize("quant", [None, "fp8", "mx", "int8"])
+def test_rmsnorm_in_place(quant):
+    """residual_out = residual and y = x, the layer's own use, against separate buffers."""
+    x, r = make(65, 1280, "bf16", 0, 4), make(65, 1280, "bf16", 0, 5)
+    g = torch.ones(1280, device="cuda")
+    y, ro = torch.empty_like(x), torch.empty_like(r)
+    c1, s1 = codes_for(quant, 65, 1280) if quant else (None, None)
+    c2, s2 = codes_for(quant, 65, 1280) if quant else (None, None)
+    kw = lambda c, s: dict(quant=quant, codes=None if c is None else c[:65], scales=s)  # noqa: E731
+    B.moe_rmsnorm(x, g, 1e-6, y=y, residual=r, residual_out=ro, **kw(c1, s1))
+    xi, ri = x.clone(), r.clone()
+    B.moe_rmsnorm(xi, g, 1e-6, y=xi, residual=ri, residual_out=ri, **kw(c2, s2))
+    torch.cuda.synchronize()
+    assert torch.equal(xi, y) and torch.equal(ri, ro)
+    if quant:
+        assert torch.equal(c1, c2) and torch.equal(s1, s2)
+
+
+def test_rmsnorm_special_rows():
+    """Zero rows, rows with an infinity or a NaN, the largest bf16 values that the sum can hold."""
+    x = torch.randn(6, 512).to(torch.bfloat16)
+    x[1] = 0
+    x[2, 100] = float("inf")
+    x[3, 5] = float("nan")
+    x[4] *= 2.0 ** 58            # squares near 2^116 * 512: inside fp32
+    x[5] *= 2.0 ** -70           # squares underflow: eps alone is left
+    x = x.cuda()
+    g = torch.ones(512, device="cuda")
+    for quant in ("fp8", "mx", "int8"):
+        y = torch.empty((6, 512), device="cuda")
+        c, s = codes_for(quant, 6, 512)
+        B.moe_rmsnorm(x, g, 1e-6, y=y, quant=quant, codes=c[:6], scales=s)
+        torch.cuda.synchronize()
+        n, _ = orc.rmsnorm(x.double().cpu().numpy()[[0, 1, 4, 5]], np.ones(512), 1e-6)
+        got = y.cpu().numpy()
+        assert (np.abs(got[[0, 1, 4, 5]] - n) <= N_TOL * np.abs(n)).all()
+        assert np.isnan(got[2]).any() and np.isnan(got[3]).all()
+        assert (got[1] == 0).all() and (c[1] == 0).all()
+        if quant == "int8":
+            sc = s.cpu().numpy()
+            assert sc[1] == 0 and not np.isfinite(sc[2]) and np.isnan(sc[3]) and np.isfinite(sc[[0, 4, 5]]).all()
+            assert (c[2] == 0).all() and (c[3] == 0).all()
+        elif quant == "fp8":
+            sc = s.cpu().numpy()
+            assert (sc[1] == 0).all() and np.isnan(sc[3]).all() and not np.isfinite(sc[2, 100 // 128])
+        else:
+            sc = mx_codes(s)
+            assert (sc[1] == 0).all() and (sc[3] == 255).all() and sc[2, 100 // 32] == 255 and (sc[[0, 4, 5]] < 255).all()
+    # eps = 0 on a zero row: the formula's 0/0
+    y = torch.empty((6, 512), device="cuda")
+    B.moe_rmsnorm(x, g, 0.0, y=y)
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[0]).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 128), (7, 2048), (83, 7168), (3, 14336), (2, 32768), (130, 384)])
+def test_quantize_int8(rows, cols):
+    print("quantize_int8", rows, cols, flush=True)
+    x = make(rows, cols, "bf16", 0, 6)
+    if rows > 2:
+        x[1] = 0
+        x[2, :] = 3.0
+        x[2, 1] = -381.0         # scale 3: every quotient is 1, -127
+    c, s = codes_for("int8", rows, cols)
+    B.moe_quantize_int8(rows, cols, x, c[:rows], s)
+    torch.cuda.synchronize()
+    check_codes("int8", x.float().cpu().numpy(), c[:rows], s)
+    assert (c[rows] == 99).all()
+
+
+def test_quantize_int8_nonfinite_and_ties():
+    x = torch.zeros(4, 128)
+    x[0, :6] = torch.tensor([127.0, 0.5, 1.5, 2.5, -0.5, -3.5])   # scale 1: ties to even
+    x[1, 3] = float("inf")
+    x[2, 3] = float("nan")
+    x[3] = 2.0 ** -130                                             # a subnormal scale
+    xb = x.to(torch.bfloat16).cuda()
+    c, s = codes_for("int8", 4, 128)
+    B.moe_quantize_int8(4, 128, xb, c[:4], s)
+    torch.cuda.synchronize()
+    assert c[0, :6].tolist() == [127, 0, 2, 2, 0, -4]
+    assert (c[1] == 0).all() and (c[2] == 0).all() and torch.isinf(s[1]) and torch.isnan(s[2])
+    assert (c[3] == 127).all()
+
+
+def test_rmsnorm_streams_and_graph():
+    """On a side stream and captured: every replay, with new inputs and eager work in between, gives
+    the eager call's bits."""
+    x, r = make(40, 896, "bf16", 0, 7), make(40, 896, "bf16", 0, 8)
+    g = make(1, 896, "f32", 0, 9)[0]
+    y, ro = torch.empty_like(x), torch.empty_like(r)
+    c, s = codes_for("int8", 40, 896)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B.moe_rmsnorm(x, g, 1e-6, y=y, residual=r, residual_out=ro, quant="int8", codes=c[:40], scales=s, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    yg, rg = torch.empty_like(x), torch.empty_like(r)
+    cg, sg = codes_for("int8", 40, 896)
+    with torch.cuda.graph(graph):
+        B.moe_rmsnorm(x, g, 1e-6, y=yg, residual=r, residual_out=rg, quant="int8", codes=cg[:40], scales=sg)
+    for k in range(4):
+        if k:
+            x.copy_(make(40, 896, "bf16", 0, 20 + k))
+            B.moe_rmsnorm(x, g, 1e-6, y=y, residual=r, residual_out=ro, quant="int8", codes=c[:40], scales=s)
+        yg.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(yg, y) and torch.equal(rg, ro) and torch.equal(cg, c) and torch.equal(sg, s), f"replay {k}"
+
+
+def test_rmsnorm_refuses_mixed_tensors():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(128, device="cuda")
+    y = torch.empty_like(x)
+    for kw in (dict(y=torch.empty(4, 128)), dict(y=y, residual=torch.zeros(4, 128)), dict(y=y, residual=x.float(), residual_out=x),
+               dict(y=y, quant="int8", codes=torch.empty_like(x, dtype=torch.uint8), scales=torch.empty(4, device="cuda")),
+               dict(y=y, quant="fp8", codes=torch.empty_like(x, dtype=torch.uint8), scales=torch.empty(3, device="cuda")),
+               dict(y=y[:3]), dict(y=y, quant="mx"), dict()):
+        with pytest.raises(B.MoEError):
+            B.moe_rmsnorm(x, g, 1e-6, **kw)
+    for w in (g[:64], g.cpu(), torch.ones(256, device="cuda")[::2]):
+        with pytest.raises(B.MoEError):
+            B.moe_rmsnorm(x, w, 1e-6, y=y)
+    B.moe_rmsnorm(x[:0], g, 1e-6, y=y[:0])       # no rows: nothing happens

@@ -1,0 +1,181 @@
+"""The int8 product, the int8 quantisation and the RMS norm on the CPU: the oracle's pins, and
+every refusal of the entry points before any device call."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from mixture_experts_layer_07_amd import binding as B
+from mixture_experts_layer_07_amd.configs import CONFIGS, INT8_CONFIGS
+from mixture_experts_layer_07_amd.inputs import expert_weights, int8_row_quantise, make_expert_weights
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+FAKE = ctypes.c_void_p(0x10000)   # never dereferenced: validation fails first
+ODD = ctypes.c_void_p(0x10004)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return B.lib()
+
+
+# ------------------------------------------------------------------------------- oracle pins
+def test_oracle_int8_rows():
+    a = np.zeros((5, 128), np.float32)
+    a[0, :4] = [127 * 0.5, -63.5, 1.25, 0.75]     # scale 0.5: 127, -127, 2.5 -> 2, 1.5 -> 2
+    a[1, :3] = [254.0, -3.0, 5.0]                 # scale 2: 127, -1.5 -> -2, 2.5 -> 2
+    a[3, 0], a[3, 1] = np.inf, 3.0
+    a[4, 7] = np.nan
+    c, s = orc.quantize_rows_int8(a)
+    assert s[:3].tolist() == [0.5, 2.0, 0.0] and np.isinf(s[3]) and np.isnan(s[4])
+    assert c[0, :5].tolist() == [127, -127, 2, 2, 0] and c[1, :4].tolist() == [127, -2, 2, 0]
+    assert not c[2:].any()
+    rng = np.random.default_rng(0)
+    q = rng.integers(-127, 128, (7, 256)).astype(np.int8)
+    q[:, 0] = 127
+    v = orc.dequantize_rows_int8(q, 2.0 ** rng.integers(-8, 8, 7))
+    c, s = orc.quantize_rows_int8(v)
+    assert (c == q).all() and (orc.dequantize_rows_int8(c, s) == v).all()
+
+
+def test_oracle_rmsnorm():
+    n, s = orc.rmsnorm([[3.0, 4.0]], [1.0, 2.0], 0.0, [[0.0, 0.0]])
+    np.testing.assert_allclose(n, [[3 / np.sqrt(12.5), 8 / np.sqrt(12.5)]], rtol=1e-15)
+    assert s.tolist() == [[3.0, 4.0]]
+    rng = np.random.default_rng(1)
+    x, r = rng.normal(size=(5, 96)), rng.normal(size=(5, 96))
+    n, s = orc.rmsnorm(x, np.ones(96), 0.0, r)
+    np.testing.assert_allclose((n * n).mean(1), 1.0, rtol=1e-14)
+    np.testing.assert_allclose(orc.rmsnorm(-7.0 * x, np.ones(96), 0.0, -7.0 * r)[0], -n, rtol=1e-14)
+    assert (orc.rmsnorm(np.zeros((1, 4)), np.ones(4), 1e-6)[0] == 0).all()
+    np.testing.assert_allclose(orc.rmsnorm([[3.0, 4.0]], [1.0, 1.0], 12.5)[0], [[0.6, 0.8]], rtol=1e-15)
+
+
+def test_int8_weights():
+    cfg = INT8_CONFIGS[9].scaled(H=256, I=128, E=2, I_shared=128)
+    w = make_expert_weights(cfg)
+    assert w["w13"].dtype == torch.int8 and w["w13_scale"].shape == (2, 256) and w["w2_scale"].shape == (2, 256)
+    c13, s13, c2, s2 = expert_weights(cfg, 1)
+    assert torch.equal(w["w13"][1], c13) and torch.equal(w["w2_scale"][1], s2)
+    assert (c13.abs().amax(1) == 127).all()
+    c, s = int8_row_quantise(torch.tensor([[254.0, -3.0, 5.0], [0.0, 0.0, 0.0]]))
+    assert c.tolist() == [[127, -2, 2], [0, 0, 0]] and s.tolist() == [2.0, 0.0]
+
+
+# ------------------------------------------------------------------------------- refusals
+def norm_cfg(**kw):
+    d = dict(rows=4, cols=256, x_dtype=1, residual_dtype=1, weight_dtype=1, y_dtype=1, quant=0, eps=1e-6, x_stride=0,
+             residual_stride=0, residual_out_stride=0, y_stride=0)
+    d.update(kw)
+    return B.MoeNormConfig(**d)
+
+
+def test_rmsnorm_refusals(lib):
+    def call(c, x=FAKE, w=FAKE, r=FAKE, ro=FAKE, y=FAKE, codes=None, scales=None):
+        return lib.moe_rmsnorm(None if c is None else ctypes.byref(c), x, w, r, ro, y, codes, scales, None)
+    assert call(None) == INVALID
+    for kw, want in [(dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(cols=32769), UNSUPPORTED),
+                     (dict(x_dtype=2), INVALID), (dict(residual_dtype=4), INVALID), (dict(weight_dtype=-1), INVALID),
+                     (dict(y_dtype=3), INVALID), (dict(quant=1), INVALID), (dict(quant=5), INVALID),
+                     (dict(eps=-1e-6), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+                     (dict(x_stride=255), INVALID), (dict(residual_stride=-256), INVALID),
+                     (dict(residual_out_stride=1), INVALID), (dict(y_stride=128), INVALID)]:
+        assert call(norm_cfg(**kw)) == want, kw
+    assert call(norm_cfg(), x=None) == INVALID and call(norm_cfg(), w=None) == INVALID
+    assert call(norm_cfg(), r=None) == INVALID                      # residual_out without residual
+    assert call(norm_cfg(), y=None) == INVALID                      # nothing to write
+    assert call(norm_cfg(), codes=FAKE, scales=FAKE) == INVALID     # codes without quant
+    for q in (2, 3, 4):
+        assert call(norm_cfg(quant=q)) == INVALID
+        assert call(norm_cfg(quant=q), codes=FAKE) == INVALID
+        assert call(norm_cfg(quant=q, cols=200), codes=FAKE, scales=FAKE) == UNSUPPORTED
+        assert call(norm_cfg(quant=q), codes=ODD, scales=FAKE) == INVALID
+    assert call(norm_cfg(rows=0)) == OK                             # nothing to do, nothing launched
+
+
+def test_quantize_int8_refusals(lib):
+    assert lib.moe_quantize_int8(4, 100, FAKE, FAKE, FAKE, None) == INVALID
+    assert lib.moe_quantize_int8(-1, 256, FAKE, FAKE, FAKE, None) == INVALID
+    assert lib.moe_quantize_int8(4, 32768 + 128, FAKE, FAKE, FAKE, None) == UNSUPPORTED
+    for k in range(3):
+        p = [FAKE] * 3
+        p[k] = None
+        assert lib.moe_quantize_int8(4, 256, *p, None) == INVALID
+    assert lib.moe_quantize_int8(0, 256, FAKE, FAKE, FAKE, None) == OK
+
+
+def test_gemm_int8_refusals(lib):
+    n = lib.moe_gemm_int8_workspace_size()
+
+    def call(E=2, rows=5, N=64, K=64, off=FAKE, x=FAKE, xs=FAKE, w=FAKE, ws_=FAKE, y=FAKE, yd=1, ws=FAKE, nb=n):
+        return lib.moe_gemm_int8(E, rows, N, K, off, x, xs, w, ws_, y, yd, ws, nb, None)
+    for kw in (dict(E=0), dict(E=257), dict(rows=-1), dict(N=0), dict(K=0), dict(yd=2), dict(off=None), dict(x=None),
+               dict(xs=None), dict(w=None), dict(ws_=None), dict(y=None), dict(ws=None), dict(x=ODD), dict(w=ODD),
+               dict(y=ODD), dict(ws=ODD)):
+        assert call(**kw) == INVALID, kw
+    for kw in (dict(K=24), dict(K=131072), dict(N=1 << 16, K=1 << 15), dict(N=(1 << 20) + 1, K=16)):
+        assert call(**kw) == UNSUPPORTED, kw
+    assert call(nb=n - 1) == WORKSPACE
+    assert call(rows=0) == OK
+
+
+def test_int8_layer_config(lib):
+    for cfg in INT8_CONFIGS.values():
+        assert lib.moe_check_config(ctypes.byref(B.make_config(cfg))) == OK
+        assert B.moe_workspace_size(cfg) >= cfg.P * max(cfg.I, cfg.I_shared) * 5
+    base = INT8_CONFIGS[9]
+    for kw in (dict(H=7000), dict(I=100), dict(I_shared=64), dict(H=32768 + 128, I=128, I_shared=0)):
+        assert lib.moe_check_config(ctypes.byref(B.make_config(base.scaled(**kw)))) == UNSUPPORTED, kw
+    c = B.make_config(base.scaled(T=64, H=256, I=128, E=16, K=4, n_group=4, topk_group=2, I_shared=128))
+    pc, n = ctypes.byref(c), B.moe_workspace_size(c)
+    assert lib.moe_permute(pc, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE, n, None) == INVALID
+    ffn = lambda xs, s13, s2, nb=n: lib.moe_expert_ffn(  # noqa: E731
+        pc, 16, 256, 128, FAKE, FAKE, xs, FAKE, s13, FAKE, s2, FAKE, FAKE, nb, None)
+    assert ffn(None, FAKE, FAKE) == INVALID and ffn(FAKE, None, FAKE) == INVALID and ffn(FAKE, FAKE, None) == INVALID
+    assert ffn(FAKE, FAKE, FAKE, n - 1) == WORKSPACE
+    # the single-launch decode layer has no int8 form
+    dec = lib.moe_layer_decode(pc, *([FAKE] * 3), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, *([FAKE] * 10), n, None)
+    assert dec == UNSUPPORTED
+
+
+def test_binding_refuses_host_and_mismatched_tensors(lib):
+    """The tensor checks come before any launch; here they meet CPU tensors, whose pointers the GPU
+    must never be given."""
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    g = torch.ones(128, dtype=torch.bfloat16)
+    with pytest.raises(B.MoEError, match="current GPU"):
+        B.moe_rmsnorm(x, g, 1e-6, y=torch.empty_like(x))
+    with pytest.raises(B.MoEError, match="quant"):
+        B.moe_rmsnorm(x, g, 1e-6, quant="int4")
+    with pytest.raises(B.MoEError, match="rows, cols"):
+        B.moe_rmsnorm(x[0], g, 1e-6)
+    xi = torch.zeros(4, 64, dtype=torch.int8)
+    with pytest.raises(B.MoEError, match="current GPU"):
+        B.moe_gemm_int8(xi, torch.ones(4), xi, torch.ones(4), torch.empty(4, 4), torch.empty(16, dtype=torch.uint8))
+
+
+def test_row_tensor_checks():
+    """Shapes, types and strides of row tensors (device-independent part of the checks)."""
+    dev = torch.device("cpu")
+    chk = lambda t, r=4, c=8: B._row_tensor("t", "x", t, r, c, dev)  # noqa: E731
+    assert chk(torch.zeros(4, 8)) == (B.MOE_F32, 8)
+    assert chk(torch.zeros(4, 12, dtype=torch.bfloat16)[:, 2:10]) == (B.MOE_BF16, 12)
+    assert chk(torch.zeros(1, 8), 1) == (B.MOE_F32, 0)
+    assert chk(torch.zeros(4, 3)[:, 1:2], 4, 1) == (B.MOE_F32, 3)
+    for bad in (torch.zeros(4, 8, dtype=torch.float16), torch.zeros(4, 9), torch.zeros(8, 4).t(),
+                torch.zeros(8).expand(4, 8), torch.zeros(4, 16)[:, ::2]):
+        with pytest.raises(B.MoEError):
+            chk(bad)
+    with pytest.raises(B.MoEError):
+        B._flat("t", "codes", torch.zeros(4, 9)[:, :8], torch.float32, 32, dev)
+
+
+def test_layer_norm_argument():
+    from mixture_experts_layer_07_amd.layer import MoELayer
+    with pytest.raises(ValueError, match="norm_weight"):
+        layer = MoELayer.__new__(MoELayer)
+        layer.norm_weight = None
+        layer.forward(torch.zeros(1), residual=torch.zeros(1))
+    assert 9 not in CONFIGS and 10 not in CONFIGS
