@@ -480,6 +480,7 @@ moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* we
   a.rows = c.rows;
   a.cols = c.cols;
   a.eps = c.eps;
+  a.inv_cols = 1.0 / c.cols;
   a.x_f32 = c.x_dtype == MOE_F32;
   a.r_f32 = c.residual_dtype == MOE_F32;
   a.y_f32 = c.y_dtype == MOE_F32;

@@ -140,6 +140,7 @@ struct NormArgs {
   int64_t x_bytes = 0, r_bytes = 0, ro_bytes = 0, y_bytes = 0;  // between rows
   int rows = 0, cols = 0;
   float eps = 0.f;
+  double inv_cols = 0.0;
   bool x_f32 = false, r_f32 = false, y_f32 = false, g_f32 = false;
 };
 hipError_t launch_rmsnorm(const NormArgs& a, int quant, hipStream_t s);

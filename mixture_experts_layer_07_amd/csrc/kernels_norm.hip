@@ -9,9 +9,11 @@
 // the store. All sums and n itself are fp32; every output is rounded once, from fp32 (the codes
 // from n, not from the rounded y: the int8 experts see no second rounding).
 //
-// The quantiser of the int8 rows needs the row's largest |n|. n is formed as (s g) * rstd, and a
-// product with a positive constant is monotone under rounding, so max |n| = max |s g| * rstd
-// exactly: sum of squares and maximum go through one workgroup reduction.
+// n is rounded once: s g is carried as an exact pair (product and fma residual), the sum of squares
+// above the thread in fp64, 1/sqrt as a pair. For the MX codes n is rounded to odd (truncated, the
+// last bit set if anything was cut off), which no later rounding to fewer bits can tell from the
+// exact value: the power-of-two scale of a block and its 32 codes then never follow an ulp of fp32
+// across a border. (An fp32 y beside MX codes is that n too: within one ulp instead of half.)
 #include "device.h"
 #include "internal.h"
 
@@ -76,16 +78,26 @@ __device__ __forceinline__ void store8(void* row, bool f32, int c, int cols, con
     }
 }
 
+// fp64 through the 32-bit cross-lane moves.
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(double, make_uint2(dpp_u32<CTRL>(u.x), dpp_u32<CTRL>(u.y)));
+}
 // Sum / maximum over a wave, the result in every lane: quad exchanges, rotations inside each row
 // of 16 lanes, the other row of the half, then the two halves.
-__device__ __forceinline__ float wave_sum_dpp(float v) {
-  v += dpp_f32<0xB1>(v);
-  v += dpp_f32<0x4E>(v);
-  v += dpp_f32<0x124>(v);
-  v += dpp_f32<0x128>(v);
-  v += __uint_as_float((uint32_t)__builtin_amdgcn_ds_swizzle((int)__float_as_uint(v), 0x401F));
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 0)) +
-         __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 32));
+__device__ __forceinline__ double wave_sum_dpp(double v) {
+  v += dpp_f64<0xB1>(v);
+  v += dpp_f64<0x4E>(v);
+  v += dpp_f64<0x124>(v);
+  v += dpp_f64<0x128>(v);
+  uint2 u = __builtin_bit_cast(uint2, v);
+  v += __builtin_bit_cast(double, make_uint2((uint32_t)__builtin_amdgcn_ds_swizzle((int)u.x, 0x401F),
+                                             (uint32_t)__builtin_amdgcn_ds_swizzle((int)u.y, 0x401F)));
+  u = __builtin_bit_cast(uint2, v);
+  const uint2 l = make_uint2((uint32_t)__builtin_amdgcn_readlane((int)u.x, 0), (uint32_t)__builtin_amdgcn_readlane((int)u.y, 0));
+  const uint2 h = make_uint2((uint32_t)__builtin_amdgcn_readlane((int)u.x, 32), (uint32_t)__builtin_amdgcn_readlane((int)u.y, 32));
+  return __builtin_bit_cast(double, l) + __builtin_bit_cast(double, h);
 }
 // (as unsigned bit patterns of non-negative floats: a NaN is the largest, so it reaches the scale)
 __device__ __forceinline__ uint32_t wave_max_dpp(uint32_t m) {
@@ -122,27 +134,58 @@ __device__ __forceinline__ void int8_store8(int8_t* row, int c, const float (&v)
   *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
 }
 
-// Row reduction over the workgroup: every thread gets the sum of `sum` and the maximum of `m`.
-// One barrier; red holds one entry per wave.
-__device__ __forceinline__ void row_reduce(float& sum, uint32_t& m, float2* red) {
-  const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+// Row reductions over the workgroup, the result in every thread: one barrier, one entry of red per
+// wave (at most 16 waves: every row of 16 lanes then reduces all of them).
+__device__ __forceinline__ double row_sum(double sum, double* red) {
+  const int nw = blockDim.x >> 6;
   sum = wave_sum_dpp(sum);
-  m = wave_max_dpp(m);
-  if (nw == 1) return;
-  if ((threadIdx.x & 63) == 0) red[wave] = make_float2(sum, __uint_as_float(m));
+  if (nw == 1) return sum;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
-  const int l = threadIdx.x & 15;  // (at most 16 waves: every row of 16 lanes reduces all of them)
-  const float2 r = l < nw ? red[l] : make_float2(0.f, 0.f);
-  sum = r.x;
-  sum += dpp_f32<0xB1>(sum);
-  sum += dpp_f32<0x4E>(sum);
-  sum += dpp_f32<0x124>(sum);
-  sum += dpp_f32<0x128>(sum);
-  m = __float_as_uint(r.y);
+  const int l = threadIdx.x & 15;
+  sum = l < nw ? red[l] : 0.0;
+  sum += dpp_f64<0xB1>(sum);
+  sum += dpp_f64<0x4E>(sum);
+  sum += dpp_f64<0x124>(sum);
+  sum += dpp_f64<0x128>(sum);
+  return sum;
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* red) {
+  const int nw = blockDim.x >> 6;
+  m = wave_max_dpp(m);
+  if (nw == 1) return m;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  const int l = threadIdx.x & 15;
+  m = l < nw ? red[l] : 0u;
   m = max(m, dpp_u32<0xB1>(m));
   m = max(m, dpp_u32<0x4E>(m));
   m = max(m, dpp_u32<0x124>(m));
   m = max(m, dpp_u32<0x128>(m));
+  return m;
+}
+
+// 1 / sqrt(v) as hi + lo: the fp32 root and one Newton step in fp64. For an argument that fp32 cannot
+// hold, an infinite or zero one, and NaN, lo is 0.
+__device__ __forceinline__ float2 inv_root(double v) {
+  const float r = 1.0f / sqrtf((float)v);
+  const double e = 1.0 - v * ((double)r * (double)r);
+  return make_float2(r, fabs(e) < 0.5 ? (float)(0.5 * (double)r * e) : 0.f);
+}
+
+// s g (rstd.x + rstd.y), rounded once: to nearest, or (ODD) to odd. The sign is that of s g (the sum
+// of the pair's terms would make a negative zero positive).
+template <bool ODD>
+__device__ __forceinline__ float normed(float s, float g, float2 rstd) {
+  const float t = s * g, t_lo = fmaf(s, g, -t);
+  if (!ODD) return copysignf(fmaf(t, rstd.x, fmaf(t_lo, rstd.x, t * rstd.y)), t);
+  const float p = t * rstd.x;
+  const float q = fmaf(t, rstd.x, -p) + fmaf(t_lo, rstd.x, t * rstd.y);
+  const float n = copysignf(p + q, t), d = q - (n - p);  // (|q| < |p|: d is the exact remainder)
+  const uint32_t b = __float_as_uint(n);
+  // an even n that is not exact: one ulp towards the remainder (an infinity or NaN has no d > 0, d < 0)
+  const bool away = (d > 0.f) == (n > 0.f);
+  return (d > 0.f || d < 0.f) && !(b & 1u) ? __uint_as_float(away ? b + 1u : b - 1u) : n;
 }
 
 // Q: 0 no codes, else the layer type whose experts read them (MOE_FP8_E4M3, MOE_MXFP4, MOE_INT8).
@@ -150,7 +193,8 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& m, float2* red)
 // 128 whenever there are codes, so the 16 lanes of a 128-channel block are all inside or all outside.
 template <int V, int Q>
 __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
-  __shared__ float2 red[16];
+  __shared__ double red[16];
+  __shared__ uint32_t redm[16];
   const int row = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
   const bool xf = a.x_f32, rf = a.r_f32;
   const uint8_t* xr = static_cast<const uint8_t*>(a.x) + (size_t)row * a.x_bytes;
@@ -171,7 +215,6 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) load8(a.g, a.g_f32, (v * nt + tid) * 8, a.cols, g[v]);
   float sum = 0.f;
-  uint32_t m = 0u;
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -181,26 +224,22 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) store8(ro, rf, (v * nt + tid) * 8, a.cols, s[v]);
   }
+  const float2 rstd = inv_root(row_sum((double)sum, red) * a.inv_cols + (double)a.eps);
+  uint32_t m = 0u;
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      s[v][j] *= g[v][j];
+      s[v][j] = normed<Q == MOE_MXFP4>(s[v][j], g[v][j], rstd);
       if (Q == MOE_INT8) m = max(m, abs_bits(s[v][j]));
     }
-  row_reduce(sum, m, red);
-  const float rstd = 1.0f / sqrtf(sum / (float)a.cols + a.eps);
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[v][j] *= rstd;
   if (a.y) {
     uint8_t* yr = static_cast<uint8_t*>(a.y) + (size_t)row * a.y_bytes;
 #pragma unroll
     for (int v = 0; v < V; ++v) store8(yr, a.y_f32, (v * nt + tid) * 8, a.cols, s[v]);
   }
   if (Q == MOE_INT8) {
-    const float scale = __uint_as_float(abs_bits(__uint_as_float(m) * rstd)) / 127.0f;
+    const float scale = __uint_as_float(row_max(m, redm)) / 127.0f;
     int8_t* cr = static_cast<int8_t*>(a.codes) + (size_t)row * a.cols;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -252,7 +291,7 @@ template <int V>
 __global__ __launch_bounds__(1024) void k_quantize_int8(const uint8_t* __restrict__ in, bool f32, int nsrc,
                                                         const int32_t* __restrict__ index, int div, int cols,
                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
-  __shared__ float2 red[16];
+  __shared__ uint32_t red[16];
   const int row = blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
   unsigned src = (unsigned)row;
   if (index) {
@@ -268,9 +307,7 @@ __global__ __launch_bounds__(1024) void k_quantize_int8(const uint8_t* __restric
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, abs_bits(s[v][j]));
-  float unused = 0.f;
-  row_reduce(unused, m, red);
-  const float scale = __uint_as_float(m) / 127.0f;
+  const float scale = __uint_as_float(row_max(m, red)) / 127.0f;
   int8_t* cr = codes + (size_t)row * cols;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -280,11 +317,13 @@ __global__ __launch_bounds__(1024) void k_quantize_int8(const uint8_t* __restric
   if (tid == 0) scales[row] = scale;
 }
 
-// Groups per thread and threads of a row of `cols` channels: one group per thread (the shortest
-// chain) while that fits a workgroup, the fewest groups that do otherwise (cols <= kMaxRowCols).
+// Groups per thread and threads of a row of `cols` channels (at most kMaxRowCols): one group per
+// thread in short rows; from 4096 channels on two, so that the CU holds twice the rows and one row's
+// reduction hides behind the others' loads (8192 x 7168 bf16 to MX: 109 us with one group per thread,
+// 102.5 with two, 117 with four; one row: no difference).
 static void row_shape(int cols, int* V, int* nt) {
   const int groups = (cols + 7) / 8;
-  int v = 1;
+  int v = groups >= 512 ? 2 : 1;
   while (groups > v * 1024) v *= 2;
   *V = v;
   *nt = ((groups + v - 1) / v + 63) / 64 * 64;

@@ -81,6 +81,24 @@ def check_values(quant, ref, codes, scales):
     assert (np.abs(v - ref) <= half * (1 + 2.0 ** -17) + 2.0 ** -17 * np.abs(ref)).all()
 
 
+def check_mx_exact(n, codes, scales, s_err):
+    """MX codes and scales are those of n in 64 bits, wherever n is not within the kernel's error of a
+    border: its statistics (the thread's fp32 sums: at most 32 terms of 2^-24, halved by the root) and,
+    for fp32 inputs, the rounding of s."""
+    err = 2.0 ** -20 + s_err
+    blocks = n.reshape(n.shape[0], -1, 32)
+    mx = np.abs(blocks).max(-1)
+    lo, hi = orc.mx_scale_code(mx * (1 - err)), orc.mx_scale_code(mx * (1 + err))
+    got = mx_codes(scales)
+    assert ((got == lo) | (got == hi)).all()
+    q = n / np.repeat(orc.e8m0_decode(got), 32, 1)
+    c = codes.cpu().numpy()
+    lo, hi = orc.e4m3_encode(q * (1 - err)), orc.e4m3_encode(q * (1 + err))
+    assert ((c == lo) | (c == hi)).all()
+    # nearly everywhere the statistics' error is far smaller: at most a handful on the other side
+    assert (c != orc.e4m3_encode(q)).sum() <= 2 + n.size * 2.0 ** -20
+
+
 # rows, cols, x, residual, y, weight, quant, pad
 CASES = [
     (1, 7168, "bf16", "bf16", "bf16", "bf16", "fp8", 0),
@@ -125,7 +143,9 @@ def test_rmsnorm(case):
     if quant:
         assert (cbuf[rows] == 99).all(), "wrote outside codes"
         check_values(quant, n, cbuf[:rows], sc)
-        if yt == "f32":
+        if quant == "mx":
+            check_mx_exact(n, cbuf[:rows], sc, 2.0 ** -23 if "f32" in (xt, rt) else 0.0)
+        elif yt == "f32":
             check_codes(quant, y.cpu().numpy(), cbuf[:rows], sc)
         # codes alone are the same codes
         c2, s2 = codes_for(quant, rows, cols)
