@@ -178,6 +178,197 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   }
 }
 
+// ============================================================================ few rows
+// A launch of at most 128 rows (a decode step of a few tokens, a dense product of one to 128 rows)
+// is a weight stream with next to no arithmetic, and too few 32 x 256 tiles to occupy the chip: one
+// token against 4096 x 7168 weights is 16 of them. Here a workgroup takes 16 weight rows (GLU: 16
+// gate rows and their 16 up rows) of one expert and all of that expert's rows: its 8 waves cut K
+// among them, each streaming its piece of the weight rows straight into MFMA operands (16x16x64: 16
+// rows of 64 bytes per load, every weight read once), and the int32 sums of the waves meet in LDS
+// atomics, exact in any order. No tile list is built: blockIdx.y counts the experts that have rows,
+// found by a ballot over the offsets.
+// The token rows are read by every workgroup. Loaded straight into operands they are bound by the
+// address unit, which moves 64-byte pieces of 16 rows at a third of the rate of whole 128-byte lines
+// (4096 x 7168 weights: 64 rows 22 us, 16 rows 11.6, one row 9.3), so each wave brings its own 128
+// bytes of every row in whole lines through a corner of the LDS that no other wave touches (11.9,
+// 8.7, 8.2 us).
+// TB: blocks of 16 rows whose sums are held; an expert with more rows takes several passes. NW: waves.
+template <bool GLU, bool OUTF32, int TB, int NW>
+__global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32_t* __restrict__ offsets, int n_rows) {
+  constexpr int G = GLU ? 2 : 1, NT = NW * 64;
+  static_assert(NW >= 4, "a ballot over 256 experts");
+  __shared__ int red[G * TB * 256];
+  __shared__ u32x4 sx_rows[NW * TB * 128];  // per wave: 16 TB rows of 128 bytes
+  __shared__ unsigned long long s_mask[4];
+  __shared__ int s_e;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int e = 0, lo = 0, hi = n_rows;
+  if (offsets) {
+    const bool act = tid < g.n_exp && min(max(offsets[tid + 1], 0), n_rows) > min(max(offsets[tid], 0), n_rows);
+    const unsigned long long mask = __ballot(act);
+    if (tid == 0) s_e = -1;
+    if (wave < 4 && lane == 0) s_mask[wave] = mask;
+    __syncthreads();
+    if (act) {
+      int rank = __popcll(mask & ((1ull << lane) - 1ull));
+      for (int w = 0; w < wave; ++w) rank += __popcll(s_mask[w]);
+      if (rank == (int)blockIdx.y) s_e = tid;
+    }
+    __syncthreads();
+    e = __builtin_amdgcn_readfirstlane(s_e);
+    if (e < 0) return;
+    lo = min(max(offsets[e], 0), n_rows);
+    hi = min(max(offsets[e + 1], 0), n_rows);
+  }
+  const int n0 = blockIdx.x * 16, K = g.K;
+  const int lr = lane & 15, lk = (lane >> 4) * 16;
+  // this lane's weight row (clamped: columns past N are not stored) and token rows
+  const uint8_t* wp = g.B + (size_t)e * g.b_exp + (size_t)min(n0 + lr, (GLU ? g.glu_I : g.Nb) - 1) * K;
+  const uint8_t* wu = GLU ? wp + (size_t)g.glu_I * K : wp;
+  for (; lo < hi; lo += 16 * TB) {
+    const int rows = min(hi - lo, 16 * TB), nb = (rows + 15) >> 4;
+    for (int i = tid; i < G * TB * 256; i += NT) red[i] = 0;
+    __syncthreads();
+    const uint8_t* xb = g.a_rows ? g.A : g.A + (size_t)lo * g.lda;
+    TileInfo ti;
+    ti.row0 = lo;
+    i32x4 acc[G][TB];
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) acc[q][t] = i32x4{0, 0, 0, 0};
+    // load instruction j: rows 8 j + lane / 8, in whole 128-byte lines; the chunk that the swizzle
+    // puts at this lane's place (16 consecutive rows then keep one chunk in 16 bank groups)
+    u32x4* sx = sx_rows + wave * TB * 128;
+    const int ch = ((lane & 7) ^ lds_swz(lane >> 3)) * 16, ch1 = ((lane & 7) ^ lds_swz(8 + (lane >> 3))) * 16;
+    uint32_t xo[2 * TB];
+#pragma unroll
+    for (int j = 0; j < 2 * TB; ++j)
+      xo[j] = (uint32_t)a_row(g, ti, min(j * 8 + (lane >> 3), rows - 1)) * (uint32_t)g.lda;
+    const int nk = (K + 127) / 128, per = (nk + NW - 1) / NW;
+    const int s0 = wave * per, s1 = min(nk, s0 + per);
+    u32x4 x[2 * TB];
+    i32x4 w[G][2];
+    // loads of 128-byte step s: chunks past K are read at the row's start (the weights there: zeros).
+    // One step ahead of the products: two or four steps ahead measured 3 to 50 % slower (registers,
+    // and waits that a conditional reload makes longer).
+    auto load = [&](int s) {
+      const int k = s * 128, k0 = k + ch < K ? k + ch : 0, k1 = k + ch1 < K ? k + ch1 : 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int kw = k + u * 64 + lk, ko = kw < K ? kw : 0;
+        w[0][u] = *reinterpret_cast<const i32x4*>(wp + ko);
+        if (GLU) w[G - 1][u] = *reinterpret_cast<const i32x4*>(wu + ko);
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * TB; ++j)
+        if (j * 8 < rows) x[j] = *reinterpret_cast<const u32x4*>(xb + (xo[j] + (uint32_t)((j & 1) ? k1 : k0)));
+    };
+    if (s0 < s1) load(s0);
+    for (int s = s0; s < s1; ++s) {
+      i32x4 v[G][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const bool in = s * 128 + u * 64 + lk < K;
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[q][u][i] = in ? w[q][u][i] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 2 * TB; ++j)
+        if (j * 8 < rows) sx[j * 64 + lane] = x[j];
+      if (s + 1 < s1) load(s + 1);
+      __builtin_amdgcn_wave_barrier();  // (this wave's own LDS traffic: in order, no workgroup barrier)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        if (t >= nb) break;  // (uniform)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const i32x4 a = __builtin_bit_cast(i32x4, sx[(t * 16 + lr) * 8 + ((u * 4 + (lane >> 4)) ^ lds_swz(lr))]);
+#pragma unroll
+          for (int q = 0; q < G; ++q) acc[q][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[q][u], a, acc[q][t], 0, 0, 0);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      if (t >= nb) break;
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) atomicAdd(&red[(q * TB + t) * 256 + i * 64 + lane], acc[q][t][i]);
+    }
+    __syncthreads();
+    // thread (t, lane): token 16 t + lane % 16, channels n0 + 4 (lane / 16) .. + 3
+    const int n = n0 + (lane >> 4) * 4;
+    for (int t = wave; t < nb; t += NW) {
+      const int tok = t * 16 + lr;
+      if (tok >= rows || n >= g.N_out) continue;
+      const float sx = g.a_scale[g.a_rows ? a_row(g, ti, tok) : lo + tok];
+      const float* sw = g.b_scale + (size_t)e * g.b_scale_exp;
+      const bool vec = (g.N_out & 3) == 0;
+      float v[4];
+      if constexpr (GLU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float gate = (float)red[t * 256 + i * 64 + lane] * (sx * sw[n + i]);
+          const float up = (float)red[(TB + t) * 256 + i * 64 + lane] * (sx * sw[g.glu_I + n + i]);
+          v[i] = silu_fast(gate) * up;
+        }
+      } else {
+        const f32x4 sn = i8::channel_scales(sw, n, g.N_out, vec);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (float)red[t * 256 + i * 64 + lane] * (sx * sn[i]);
+      }
+      uint8_t* row = g.C + (size_t)(lo + tok) * g.ldc;
+      if (vec) {
+        if constexpr (OUTF32)
+          *reinterpret_cast<float4*>(row + (size_t)n * 4) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(row + (size_t)n * 2) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < g.N_out) {
+            if constexpr (OUTF32)
+              reinterpret_cast<float*>(row)[n + i] = v[i];
+            else
+              reinterpret_cast<uint16_t*>(row)[n + i] = (uint16_t)bf16x2(v[i], 0.f);
+          }
+      }
+    }
+    __syncthreads();  // (red is read before the next pass clears it)
+  }
+}
+
+// Launches of up to this many rows take k_gemm_i8_few: at 128 rows of one expert 19 us against 38 for
+// the 32 x 256 tiles (4096 x 7168 weights), over 64 experts 342 against 340.
+constexpr int kFewRows = 128;
+
+// Row blocks: as many as the rows fill, two where they are spread over experts (64 rows of 64 experts:
+// 340 us with two blocks, 597 with eight). Eight blocks leave one workgroup per CU by their LDS: four
+// waves each where the grid is larger than the chip (128 x 7168 x 2048: 13.8 us, 15.8 with eight
+// waves), eight where it is not (128 x 4096 x 7168: 19.5 us, 29 with four).
+template <bool GLU, bool OUTF32>
+static hipError_t launch_few(const char* name, const GemmArgs& g, const int32_t* offsets, int n_rows, hipStream_t s) {
+  const dim3 grid((g.N_out + 15) / 16, offsets ? (n_rows < g.n_exp ? n_rows : g.n_exp) : 1);
+  return timed_launch(name, s, [&] {
+    if (n_rows <= 16)
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 1, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+    else if (n_rows <= 32 || g.n_exp > 1)
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 2, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+    else if (n_rows <= 64)
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 4, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+    else if ((int)grid.x > dev_info().cus)
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 4>), grid, dim3(256), 0, s, g, offsets, n_rows);
+    else
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+  });
+}
+
 static int round8(int v) { return ((v + 7) / 8) * 8; }
 
 template <class K>
@@ -225,6 +416,9 @@ hipError_t launch_int8_gemm(const Int8GemmArgs& a, hipStream_t s) {
   g.K = a.K;
   g.N_out = g.Nb = a.N;
   g.n_tiles_n = (a.N + 255) / 256;
+  if (a.n_rows <= kFewRows)
+    return a.y_f32 ? launch_few<false, true>("gemm_i8_f32out_few", g, a.offsets, a.n_rows, s)
+                   : launch_few<false, false>("gemm_i8_few", g, a.offsets, a.n_rows, s);
   const bool large = large_tiles(a.n_rows, a.n_exp, g.n_tiles_n, cus);
   hipError_t e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s);
   if (e != hipSuccess) return e;
@@ -272,16 +466,18 @@ hipError_t launch_expert_ffn_int8(const FfnArgs& a, hipStream_t s) {
   g2.K = I;
   g2.N_out = g2.Nb = H;
   g2.n_tiles_n = (H + 255) / 256;
-  const bool large = large_tiles(a.n_rows, a.n_exp, g1.n_tiles_n, cus);
+  const bool few = a.n_rows <= kFewRows, large = large_tiles(a.n_rows, a.n_exp, g1.n_tiles_n, cus);
   const int grid = round8(large ? cus : cus * 2);
   hipError_t e;
-  if ((e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s)) != hipSuccess) return e;
-  e = large ? launch_one("gemm_i8_gateup_swiglu", k_gemm_i8_w4<true, true>, grid, g1, s)
-            : launch_one("gemm_i8_gateup_swiglu_m32", k_gemm_i8_m32<true, true>, grid, g1, s);
+  if (!few && (e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s)) != hipSuccess) return e;
+  e = few     ? launch_few<true, true>("gemm_i8_gateup_swiglu_few", g1, a.offsets, a.n_rows, s)
+      : large ? launch_one("gemm_i8_gateup_swiglu", k_gemm_i8_w4<true, true>, grid, g1, s)
+              : launch_one("gemm_i8_gateup_swiglu_m32", k_gemm_i8_m32<true, true>, grid, g1, s);
   if (e != hipSuccess) return e;
   if ((e = launch_quantize_int8("requantize_int8", a.h, true, a.n_rows, a.n_rows, nullptr, 1, I, a.h_codes,
                                 static_cast<float*>(a.h_scale), s)) != hipSuccess)
     return e;
+  if (few) return launch_few<false, false>("gemm_i8_down_few", g2, a.offsets, a.n_rows, s);
   return large ? launch_one("gemm_i8_down", k_gemm_i8_w4<false, false>, grid, g2, s)
                : launch_one("gemm_i8_down_m32", k_gemm_i8_m32<false, false>, grid, g2, s);
 }

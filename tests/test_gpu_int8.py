@@ -67,6 +67,8 @@ PRODUCTS = [
     ([700], 1000, 640, False), ([5000], 3004, 768, False), ([4999], 4099, 1040, False), ([4100], 4096, 400, True),
     ([0, 5, 0, 0, 70, 1], 300, 320, False), ([0, 0, 0], 64, 64, False), ([300, 0, 1, 900, 17, 256], 4096, 1296, False),
     ([1] * 64, 512, 2048, False), ([0] * 255 + [9], 128, 176, True), ([4, 12, 0, 33] * 20, 513, 3584, False),
+    ([128], 4352, 272, False), ([100], 4129, 1920, True), ([65], 96, 4112, False), ([17, 40, 0, 50], 80, 464, True),
+    ([97, 0, 3], 200, 7168, False), ([16], 7168, 2048, False), ([0, 0, 64], 33, 1024, True),
     ([520, 1, 600, 255, 257, 128, 64, 2000], 2048, 32, True), ([12], 256, 14336, False), ([257, 300], 12290, 208, False),
 ]
 
@@ -184,6 +186,7 @@ LAYERS = {
     "dsv3": BASE.scaled(T=520, H=256, I=256, E=32, K=8, I_shared=384),
     "decode": BASE.scaled(T=40, H=512, I=128, E=64, K=8, I_shared=256),
     "one-token": BASE.scaled(T=1, H=384, I=640, E=16, K=4, n_group=4, topk_group=2, I_shared=128),
+    "few-rows": BASE.scaled(T=25, H=640, I=384, E=12, K=5, n_group=1, topk_group=1, I_shared=128),
     "mixtral": BASE.scaled(T=1100, H=384, I=1152, E=8, K=2, n_group=1, topk_group=1, score="softmax", route_scale=1.0,
                            bias=None, I_shared=0, out="f32"),
     "large-tiles": BASE.scaled(T=2100, H=512, I=2048, E=4, K=2, n_group=1, topk_group=1, I_shared=2048),
