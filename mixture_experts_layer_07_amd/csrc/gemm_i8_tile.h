@@ -92,76 +92,85 @@ __device__ __forceinline__ f32x4 channel_scales(const float* sw, int n, int Nb, 
 // grid in a share of cases that costs about 0.7 % of rms in Linear-2's output, four times what
 // the output's own bf16 rounding does.)
 // Else: y rows, bf16 (rounded once) or fp32.
+// s_xs, s_ws: the scales of the tile's rows and of its 256 weight rows, in the LDS.
+// The values go to memory through st, a part of the LDS that only this wave uses (the K loop's
+// stages; every wave is past them): a lane's own values are 8 or 16 bytes of one row, and stored as
+// they are each instruction touches 32 rows, which took 20 us per 256 x 256 tile; read back from
+// the LDS it writes 4 or 8 rows of 256 or 128 whole bytes. Chunks of 16 bytes are swizzled so that
+// the 32 rows written at once spread over the banks.
 template <int MB, int NB, bool GLU, bool OUTF32>
 __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, const i32x16 (&acc)[MB][NB],
-                                         const float* s_xs, int r0, int c0, int lane) {
+                                         const float* s_xs, const float* s_ws, u32x4* st, int r0, int c0, int lane) {
+  constexpr bool F32 = GLU || OUTF32;
+  constexpr int ES = F32 ? 4 : 2, EPC = 16 / ES;            // bytes per value, values per chunk
+  constexpr int PASSES = !GLU && OUTF32 && NB == 4 ? 2 : 1;  // (st holds 256 bytes of every row)
+  constexpr int NBP = NB / PASSES, COLS = GLU ? NB * 16 : NBP * 32, CH = COLS / EPC;
+  static_assert(CH == 8 || CH == 16, "rows of 128 or 256 bytes");
+  constexpr int RPI = 64 / CH;  // rows per store instruction
   const int lrow = lane & 31, lk = lane >> 5;
   const int ldc = (int)g.ldc;
   const int row0 = __builtin_amdgcn_readfirstlane(ti.row0), mvalid = __builtin_amdgcn_readfirstlane(ti.mvalid);
   const __amdgpu_buffer_rsrc_t rc =
       __builtin_amdgcn_make_buffer_rsrc(g.C + (size_t)row0 * g.ldc, (short)0, mvalid * ldc, 0x00020000);
-  const float* sw = g.b_scale + (size_t)ti.e * g.b_scale_exp;
-  int rbase = r0 + lrow;
-  asm volatile("" : "+v"(rbase));  // (row offsets formed here, not held across the K loop)
-  if constexpr (GLU) {
+  auto swz = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
 #pragma unroll
-    for (int q = 0; q < NB / 2; ++q)
+  for (int pass = 0; pass < PASSES; ++pass) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = ti.nt * 128 + c0 / 2 + q * 32 + j * 8 + lk * 4;
-        const f32x4 sg = *reinterpret_cast<const f32x4*>(sw + n);
-        const f32x4 su = *reinterpret_cast<const f32x4*>(sw + g.glu_I + n);
+    for (int mb = 0; mb < MB; ++mb) {
+      const int row = mb * 32 + lrow;
+      const float sx = s_xs[r0 + row];
+      u32x4* dst = st + row * CH;
+      const int sw = swz(row);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          const float sx = s_xs[rbase + mb * 32];
-          u32x4 h;
+      for (int q = 0; q < (GLU ? NB / 2 : NBP); ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float gate = (float)acc[mb][2 * q][4 * j + i] * (sx * sg[i]);
-            const float up = (float)acc[mb][2 * q + 1][4 * j + i] * (sx * su[i]);
-            h[i] = __float_as_uint(silu_fast(gate) * up);
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(h, rc, (rbase + mb * 32) * ldc + n * 4, 0, 0);
-        }
-      }
-  } else {
-    const bool vec = (g.N_out & 3) == 0;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = ti.nt * 256 + c0 + nb * 32 + j * 8 + lk * 4;
-        const f32x4 sn = channel_scales(sw, n, g.N_out, vec);
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          const float sx = s_xs[rbase + mb * 32];
+        for (int j = 0; j < 4; ++j) {
           float v[4];
+          if constexpr (GLU) {
+            const f32x4 sg = *reinterpret_cast<const f32x4*>(s_ws + c0 + q * 64 + j * 8 + lk * 4);
+            const f32x4 su = *reinterpret_cast<const f32x4*>(s_ws + c0 + q * 64 + 32 + j * 8 + lk * 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = (float)acc[mb][nb][4 * j + i] * (sx * sn[i]);
-          const int off = (rbase + mb * 32) * ldc + n * (OUTF32 ? 4 : 2);
-          if (vec) {
-            if (n < g.N_out) {
-              if constexpr (OUTF32) {
-                const u32x4 u = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-                __builtin_amdgcn_raw_buffer_store_b128(u, rc, off, 0, 0);
-              } else {
-                typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-                const u32x2 u = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
-                __builtin_amdgcn_raw_buffer_store_b64(u, rc, off, 0, 0);
-              }
+            for (int i = 0; i < 4; ++i) {
+              const float gate = (float)acc[mb][2 * q][4 * j + i] * (sx * sg[i]);
+              v[i] = silu_fast(gate) * ((float)acc[mb][2 * q + 1][4 * j + i] * (sx * su[i]));
             }
           } else {
+            const int nb = pass * NBP + q;
+            const f32x4 sn = *reinterpret_cast<const f32x4*>(s_ws + c0 + nb * 32 + j * 8 + lk * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (n + i < g.N_out) {
-                if constexpr (OUTF32)
-                  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), rc, off + i * 4, 0, 0);
-                else
-                  __builtin_amdgcn_raw_buffer_store_b16((short)(bf16x2(v[i], 0.f) & 0xFFFF), rc, off + i * 2, 0, 0);
-              }
+            for (int i = 0; i < 4; ++i) v[i] = (float)acc[mb][nb][4 * j + i] * (sx * sn[i]);
           }
+          if constexpr (F32)
+            dst[(q * 8 + j * 2 + lk) ^ sw] =
+                u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+          else
+            reinterpret_cast<uint2*>(dst + ((q * 4 + j) ^ sw))[lk] = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
         }
+    }
+    __builtin_amdgcn_wave_barrier();  // (this wave's own LDS traffic: in order)
+    const int c = lane & (CH - 1);
+    const int n = (GLU ? ti.nt * 128 + c0 / 2 : ti.nt * 256 + c0 + pass * COLS) + c * EPC;
+    int rbase = lane / CH;
+    asm volatile("" : "+v"(rbase));  // (row offsets formed here, not held across the K loop)
+#pragma unroll
+    for (int i = 0; i < MB * 32 / RPI; ++i) {
+      const int row = rbase + i * RPI;
+      const u32x4 v = st[row * CH + (c ^ swz(row))];
+      const int off = (r0 + row) * ldc + n * ES;
+      if (GLU || (n + EPC <= g.N_out && (F32 || !(g.N_out & 1)))) {  // (rows are 4-byte aligned)
+        __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, 0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < EPC; ++k)
+          if (n + k < g.N_out) {
+            if constexpr (F32)
+              __builtin_amdgcn_raw_buffer_store_b32(v[k], rc, off + k * 4, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b16((short)(v[k >> 1] >> (16 * (k & 1))), rc, off + k * 2, 0, 0);
+          }
       }
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 }  // namespace i8
@@ -286,7 +295,10 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
           i8::add_partial(g.part + (size_t)(w.first + pc) * kPartStride, acc, tid);              \
       }                                                                                          \
     }                                                                                            \
-    if (store) i8::epilogue<MB_, NB_, GLU, OUTF32>(g, ti, acc, s_xs, r0, c0, lane);              \
+    if (store) {                                                                                 \
+      __syncthreads(); /* (every wave is past the stages) */                                     \
+      i8::epilogue<MB_, NB_, GLU, OUTF32>(g, ti, acc, s_xs, s_ws, st, r0, c0, lane);             \
+    }                                                                                            \
   }
 
 }  // namespace moe

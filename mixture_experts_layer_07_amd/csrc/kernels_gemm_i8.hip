@@ -52,6 +52,8 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
   __shared__ u32x4 sB0[w4::kStageB];
   __shared__ u32x4 sB1[w4::kStageB];
   __shared__ float s_xs[BM];
+  __shared__ f32x4 s_ws4[BN / 4];
+  float* s_ws = reinterpret_cast<float*>(s_ws4);
   __shared__ int tp[kMaxExperts + 1];
   __shared__ int s_slot[1 + kQueues];
   const int tid = threadIdx.x;
@@ -100,8 +102,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
         sA1[i] = z;
       }
     }
-    // the rows' token scales, for the epilogue (read after the K loop's barriers)
+    // the scales of the tile's rows and weight rows, for the epilogue (read after the K loop's barriers)
+    s_ws[tid] = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
     if (tid < ti.mvalid) s_xs[tid] = g.a_scale[g.a_rows ? a_row(g, ti, tid) : ti.row0 + tid];
+    u32x4* st = wave == 0 ? sA0 : (wave == 1 ? sA1 : (wave == 2 ? sB0 : sB1));  // the epilogue's 32 KB of this wave
     // K pieces always take the 2 x 2 layout (their partial tiles share one shape)
     if (w.piece >= 0 || ti.mvalid > 128) {
       MOE_I8_TILE(4, 4, (wave >> 1) * 128, (wave & 1) * 128, true)
@@ -125,6 +129,8 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   __shared__ u32x4 sB0[w4::kStageB];
   __shared__ u32x4 sB1[w4::kStageB];
   __shared__ float s_xs[BM];
+  __shared__ f32x4 s_ws4[BN / 4];
+  float* s_ws = reinterpret_cast<float*>(s_ws4);
   __shared__ int tp[kMaxExperts + 1];
   __shared__ int s_slot[1 + kQueues];
   for (int i = threadIdx.x; i <= g.n_exp; i += 256) tp[i] = g.tp[i];
@@ -173,7 +179,9 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
         sA1[i] = z;
       }
     }
+    s_ws[tid] = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
     if (tid < ti.mvalid) s_xs[tid] = g.a_scale[g.a_rows ? a_row(g, ti, tid) : ti.row0 + tid];
+    u32x4* st = sB0 + wave * 512;  // the epilogue's 8 KB of this wave
     MOE_I8_TILE(1, 2, 0, wave * 64, true)
   }
 }
