@@ -47,8 +47,55 @@ __device__ __forceinline__ void mfmas(i32x16 (&acc)[MB][NB], const i32x4 (&a)[MB
 }  // namespace w4
 
 namespace i8 {
+// What a tile waits for before its first loads leave is paid once per tile (42 tiles per CU in a
+// DeepSeek-V3-shaped Linear-2 of 16 steps each), so: the group offsets are read from a copy in the LDS
+// (so), the scales go to the LDS only after the first loads are issued, and the next item is claimed
+// four steps before this one ends.
+
+// decode_tile with the group offsets in the LDS.
+__device__ __forceinline__ TileInfo decode(int t, const int* tp, const int* so, int n_exp, int n_tiles_n, int BM) {
+  TileInfo ti;
+  t = __builtin_amdgcn_readfirstlane(t);
+  const int q = t / n_tiles_n;
+  int lo = 0, hi = n_exp - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__builtin_amdgcn_readfirstlane(tp[mid]) <= q)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int tp0 = __builtin_amdgcn_readfirstlane(tp[lo]);
+  const int mcount = __builtin_amdgcn_readfirstlane(tp[lo + 1]) - tp0;
+  const int local = t - tp0 * n_tiles_n;
+  ti.e = lo;
+  ti.nt = local / mcount;
+  ti.mt = local - ti.nt * mcount;
+  ti.row0 = __builtin_amdgcn_readfirstlane(so[lo]) + ti.mt * BM;
+  const int mv = __builtin_amdgcn_readfirstlane(so[lo + 1]) - ti.row0;
+  ti.mvalid = mv < BM ? mv : BM;
+  return ti;
+}
+
+// The item after one whose claim (a draw from the own range, made by thread 0 while that item ran) is
+// given; with `own` cleared, next_item's other ranges.
+__device__ __forceinline__ WorkItem claimed_item(const GemmArgs& g, const SplitQueue& sq, int claim, int total, int KT,
+                                                 int min_steps, int max_slots, int* s_slot, bool& own) {
+  if (own) {
+    if (threadIdx.x == 0) s_slot[0] = claim;
+    __syncthreads();
+    const int it = __builtin_amdgcn_readfirstlane(s_slot[0]);
+    __syncthreads();
+    const WorkItem w = plan_item(sq, it, KT);
+    if (w.tile >= 0) return w;
+    own = false;
+    range_items(total, KT, min_steps, max_slots, s_slot);
+  }
+  return next_item(g, sq, total, KT, min_steps, max_slots, s_slot, own);
+}
+
 // Partial tiles of K pieces: int32 sums, exact in any order.
-template <int MB, int NB>
+template <int MB, int NB, int NT = 256>
 __device__ __forceinline__ void store_partial(float* part, const i32x16 (&acc)[MB][NB], int tid) {
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
@@ -57,10 +104,10 @@ __device__ __forceinline__ void store_partial(float* part, const i32x16 (&acc)[M
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const i32x4 v = {acc[mb][nb][4 * c], acc[mb][nb][4 * c + 1], acc[mb][nb][4 * c + 2], acc[mb][nb][4 * c + 3]};
-        reinterpret_cast<i32x4*>(part)[((mb * NB + nb) * 4 + c) * 256 + tid] = v;
+        reinterpret_cast<i32x4*>(part)[((mb * NB + nb) * 4 + c) * NT + tid] = v;
       }
 }
-template <int MB, int NB>
+template <int MB, int NB, int NT = 256>
 __device__ __forceinline__ void add_partial(const float* part, i32x16 (&acc)[MB][NB], int tid) {
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
@@ -68,7 +115,7 @@ __device__ __forceinline__ void add_partial(const float* part, i32x16 (&acc)[MB]
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const i32x4 v = reinterpret_cast<const i32x4*>(part)[((mb * NB + nb) * 4 + c) * 256 + tid];
+        const i32x4 v = reinterpret_cast<const i32x4*>(part)[((mb * NB + nb) * 4 + c) * NT + tid];
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mb][nb][4 * c + e] += v[e];
       }
@@ -84,7 +131,7 @@ __device__ __forceinline__ f32x4 channel_scales(const float* sw, int n, int Nb, 
   return v;
 }
 
-// Epilogue of a wave's MB x NB blocks at rows r0.., weight rows c0.. of the 256-row weight tile. In a
+// Epilogue of a wave's MB x NB blocks at rows r0.., weight rows c0.. of the BN-row weight tile. In a
 // 32x32 block lane l holds token l & 31, channels 8 (i / 4) + 4 (l / 32) + i % 4.
 // The int32 sum is rounded to fp32 (2^-24 of it) and multiplied by the two scales in fp32.
 // GLU: blocks 2q, 2q+1 hold gate and up of the same channels; SiLU(gate) * up is kept in fp32. (It is
@@ -92,13 +139,13 @@ __device__ __forceinline__ f32x4 channel_scales(const float* sw, int n, int Nb, 
 // grid in a share of cases that costs about 0.7 % of rms in Linear-2's output, four times what
 // the output's own bf16 rounding does.)
 // Else: y rows, bf16 (rounded once) or fp32.
-// s_xs, s_ws: the scales of the tile's rows and of its 256 weight rows, in the LDS.
+// s_xs, s_ws: the scales of the tile's rows and of its BN weight rows, in the LDS.
 // The values go to memory through st, a part of the LDS that only this wave uses (the K loop's
 // stages; every wave is past them): a lane's own values are 8 or 16 bytes of one row, and stored as
 // they are each instruction touches 32 rows, which took 20 us per 256 x 256 tile; read back from
 // the LDS it writes 4 or 8 rows of 256 or 128 whole bytes. Chunks of 16 bytes are swizzled so that
 // the 32 rows written at once spread over the banks.
-template <int MB, int NB, bool GLU, bool OUTF32>
+template <int MB, int NB, bool GLU, bool OUTF32, int BN>
 __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, const i32x16 (&acc)[MB][NB],
                                          const float* s_xs, const float* s_ws, u32x4* st, int r0, int c0, int lane) {
   constexpr bool F32 = GLU || OUTF32;
@@ -149,7 +196,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
     }
     __builtin_amdgcn_wave_barrier();  // (this wave's own LDS traffic: in order)
     const int c = lane & (CH - 1);
-    const int n = (GLU ? ti.nt * 128 + c0 / 2 : ti.nt * 256 + c0 + pass * COLS) + c * EPC;
+    const int n = (GLU ? ti.nt * (BN / 2) + c0 / 2 : ti.nt * BN + c0 + pass * COLS) + c * EPC;
     int rbase = lane / CH;
     asm volatile("" : "+v"(rbase));  // (row offsets formed here, not held across the K loop)
 #pragma unroll
@@ -197,74 +244,101 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
 #define MOE_I8_BDMA(stage, kk)                                                                   \
   do {                                                                                           \
     const uint32_t ko_ = MOE_I8_KOFF(kk);                                                        \
-    _Pragma("unroll") for (int j_ = 0; j_ < 8; ++j_)                                             \
+    _Pragma("unroll") for (int j_ = 0; j_ < BJ; ++j_)                                            \
         dma_to_lds<16>(Be + (uint32_t)(ob[j_] + ko_), (stage) + j_ * 256 + wave * 64);           \
   } while (0)
 // Zeros instead of this lane's weights of step kk where its chunk lies past K.
 #define MOE_I8_MASK(R, kk)                                                                       \
   do {                                                                                           \
     if ((int)(kk) * 128 > kmax) {                                                                \
-      _Pragma("unroll") for (int j_ = 0; j_ < 8; ++j_) R[j_] = u32x4{0u, 0u, 0u, 0u};            \
+      _Pragma("unroll") for (int j_ = 0; j_ < BJ; ++j_) R[j_] = u32x4{0u, 0u, 0u, 0u};           \
     }                                                                                            \
   } while (0)
 
-// One step on stage (ca, cb), as MOE_W4_STEP with the loads above.
+#define MOE_I8_BWRITE(stage, R)                                                                  \
+  do {                                                                                           \
+    _Pragma("unroll") for (int j_ = 0; j_ < BJ; ++j_) (stage)[bw_off + j_ * 256] = R[j_];         \
+  } while (0)
+// After the barrier: MFMAs carry the next fragments' reads, then the weight writes and A loads.
+#define MOE_I8_POST(MB_, NB_, W, NEXT)                                                           \
+  {                                                                                              \
+    constexpr int nm_ = (MB_) * (NB_);                                                           \
+    constexpr int nr_ = (NEXT) ? ((MB_) + (NB_) < nm_ ? (MB_) + (NB_) : nm_) : 0;                \
+    constexpr int nw_ = (W) ? BJ : 0;                                                            \
+    _Pragma("unroll") for (int i_ = 0; i_ < nr_; ++i_) {                                         \
+      MOE_SGB(0x008, 1);                                                                         \
+      MOE_SGB(0x100, 1);                                                                         \
+    }                                                                                            \
+    _Pragma("unroll") for (int i_ = 0; i_ < nw_; ++i_) {                                         \
+      if (nr_ + i_ < nm_) MOE_SGB(0x008, 1);                                                     \
+      MOE_SGB(0x200, 1);                                                                         \
+      if (i_ < AJ) MOE_SGB(0x010, 1);                                                            \
+    }                                                                                            \
+    if (nr_ + nw_ < nm_) MOE_SGB(0x008, nm_ - nr_ - nw_);                                        \
+  }
+
+// One step on stage (ca, cb), as MOE_W4_STEP with the loads above. BJ (in scope): weight loads per
+// lane and step, 3/8 of them in each of the first two sub-steps and the rest in the third.
 #define MOE_I8_STEP(MB_, NB_, ca, cb, na, nb, k, LB, W, NEXT, RW, RL)                           \
   w4::frags<MB_, NB_>(ca, cb, 1, r0, c0, lane, a1, b1);                                          \
-  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 0, 3);                                                       \
+  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 0, L1_);                                                       \
   w4::mfmas<MB_, NB_>(acc, a0, b0);                                                              \
-  MOE_W4_SUBL(MB_, NB_, LB, 3)                                                                   \
+  MOE_W4_SUBL(MB_, NB_, LB, L1_)                                                                   \
   w4::frags<MB_, NB_>(ca, cb, 2, r0, c0, lane, a0, b0);                                          \
-  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 3, 6);                                                       \
+  if (LB) MOE_I8_BLOAD(RL, (k) + 3, L1_, 2 * L1_);                                                       \
   w4::mfmas<MB_, NB_>(acc, a1, b1);                                                              \
-  MOE_W4_SUBL(MB_, NB_, LB, 3)                                                                   \
+  MOE_W4_SUBL(MB_, NB_, LB, L1_)                                                                   \
   w4::frags<MB_, NB_>(ca, cb, 3, r0, c0, lane, a1, b1);                                          \
-  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 6, 8);                                                       \
+  if (LB) MOE_I8_BLOAD(RL, (k) + 3, 2 * L1_, BJ);                                                       \
   w4::mfmas<MB_, NB_>(acc, a0, b0);                                                              \
-  MOE_W4_SUBL(MB_, NB_, LB, 2)                                                                   \
+  MOE_W4_SUBL(MB_, NB_, LB, BJ - 2 * L1_)                                                                   \
   /* own fragment reads and weight writes done, A of step k+1 landed (only this step's weight \
      loads may be outstanding); the barrier extends both to all waves */                       \
-  __builtin_amdgcn_s_waitcnt((LB) ? kWaitLgkm0Vm8 : kWaitLgkm0Vm0);                              \
+  __builtin_amdgcn_s_waitcnt((LB) ? wait_lgkm0_vm(BJ) : kWaitLgkm0Vm0);                              \
   __builtin_amdgcn_s_barrier();                                                                  \
   __builtin_amdgcn_sched_barrier(0);                                                             \
   if (NEXT) w4::frags<MB_, NB_>(na, nb, 0, r0, c0, lane, a0, b0);                                \
   if (W) {                                                                                       \
-    MOE_W4_BWRITE(cb, RW);                                                                       \
+    MOE_I8_BWRITE(cb, RW);                                                                       \
     MOE_I8_ALOADS(ca, (k) + 2, AJ);                                                              \
   }                                                                                              \
   w4::mfmas<MB_, NB_>(acc, a1, b1);                                                              \
-  MOE_W4_POST(MB_, NB_, W, NEXT)                                                                 \
+  MOE_I8_POST(MB_, NB_, W, NEXT)                                                                 \
   __builtin_amdgcn_sched_barrier(0);
 
+// ws_r, xs_r: this thread's weight row and token scale.
 // One tile (or K piece of a tile) with waves of MB x NB blocks: rows r0.., weight rows c0... tail:
 // whether steps [k0, k1) reach past the K / 128 full steps (uniform; then at most the last two do).
 #define MOE_I8_TILE(MB_, NB_, r0_, c0_, SPLIT)                                                   \
   {                                                                                              \
     const int r0 = (r0_), c0 = (c0_);                                                            \
-    constexpr int AJ = (MB_) * (NB_) == 16 ? 8 : (MB_); /* A load instructions per wave, step */ \
+    constexpr int AJ = AJT == 4 ? 4 : ((MB_) * (NB_) == 16 ? 8 : (MB_)); /* A loads per wave, step */ \
+    constexpr int L1_ = (BJ * 3 + 7) / 8;                                                        \
     i32x16 acc[MB_][NB_];                                                                        \
     _Pragma("unroll") for (int mb = 0; mb < (MB_); ++mb)                                         \
       _Pragma("unroll") for (int nb = 0; nb < (NB_); ++nb)                                       \
         _Pragma("unroll") for (int i = 0; i < 16; ++i) acc[mb][nb][i] = 0;                       \
-    u32x4 RB0[8], RB1[8];                                                                        \
+    u32x4 RB0[BJ], RB1[BJ];                                                                      \
     MOE_I8_ALOADS(sA0, k0, AJ);                                                                  \
     MOE_I8_BDMA(sB0, k0);                                                                        \
     MOE_I8_ALOADS(sA1, k0 + 1, AJ);                                                              \
     MOE_I8_BDMA(sB1, k0 + 1);                                                                    \
     /* (a two-step tile loads step k0+1 again: unused, keeps the wait count fixed) */           \
-    MOE_I8_BLOAD(RB0, k0 + 2 < k1 ? k0 + 2 : k1 - 1, 0, 8);                                      \
+    MOE_I8_BLOAD(RB0, k0 + 2 < k1 ? k0 + 2 : k1 - 1, 0, BJ);                                     \
+    s_ws[tid] = ws_r;                                                                            \
+    if (tid < ti.mvalid) s_xs[tid] = xs_r;                                                       \
     if (tail && k0 + 2 == k1) {                                                                  \
       /* both steps came by direct-to-LDS loads: zeros over this lane's chunks past K */         \
       __builtin_amdgcn_s_waitcnt(kWaitLgkm0Vm0);                                                 \
       const u32x4 z_ = {0u, 0u, 0u, 0u};                                                         \
-      _Pragma("unroll") for (int j_ = 0; j_ < 8; ++j_) {                                         \
+      _Pragma("unroll") for (int j_ = 0; j_ < BJ; ++j_) {                                        \
         if (k0 * 128 > kmax) sB0[bw_off + j_ * 256] = z_;                                        \
         if ((k0 + 1) * 128 > kmax) sB1[bw_off + j_ * 256] = z_;                                  \
       }                                                                                          \
       __syncthreads();                                                                           \
     }                                                                                            \
     /* step k0 landed (step k0+1 and the weights of k0+2 may still be in flight) */             \
-    __builtin_amdgcn_s_waitcnt(wait_lgkm0_vm(AJ + 16));                                          \
+    __builtin_amdgcn_s_waitcnt(wait_lgkm0_vm(AJ + 2 * BJ));                                          \
     __builtin_amdgcn_s_barrier();                                                                \
     i32x4 a0[MB_], b0[NB_], a1[MB_], b1[NB_];                                                    \
     w4::frags<MB_, NB_>(sA0, sB0, 0, r0, c0, lane, a0, b0);                                      \
@@ -273,6 +347,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
       MOE_I8_STEP(MB_, NB_, sA0, sB0, sA1, sB1, k, true, true, true, RB0, RB1)                   \
       MOE_I8_STEP(MB_, NB_, sA1, sB1, sA0, sB0, k + 1, true, true, true, RB1, RB0)               \
     }                                                                                            \
+    if (own && tid == 0) claim = atomicAdd(&g.queue[sq.q], 1);                                   \
     if (k + 4 == k1) {                                                                           \
       if (tail) MOE_I8_MASK(RB0, k + 2);                                                         \
       MOE_I8_STEP(MB_, NB_, sA0, sB0, sA1, sB1, k, true, true, true, RB0, RB1)                   \
@@ -297,7 +372,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
     }                                                                                            \
     if (store) {                                                                                 \
       __syncthreads(); /* (every wave is past the stages) */                                     \
-      i8::epilogue<MB_, NB_, GLU, OUTF32>(g, ti, acc, s_xs, s_ws, st, r0, c0, lane);             \
+      i8::epilogue<MB_, NB_, GLU, OUTF32, BN>(g, ti, acc, s_xs, s_ws, st, r0, c0, lane);         \
     }                                                                                            \
   }
 

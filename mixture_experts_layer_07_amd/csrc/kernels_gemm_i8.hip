@@ -7,6 +7,7 @@
 // in fp32), the per-row requantisation, Linear-2. Tile list, ranges and K pieces as for the other
 // types (gemm_common.h).
 #include "gemm_i8_tile.h"
+#include <math.h>
 
 namespace moe {
 
@@ -55,22 +56,28 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
   __shared__ f32x4 s_ws4[BN / 4];
   float* s_ws = reinterpret_cast<float*>(s_ws4);
   __shared__ int tp[kMaxExperts + 1];
+  __shared__ int so[kMaxExperts + 1];
   __shared__ int s_slot[1 + kQueues];
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int i = tid; i <= g.n_exp; i += 256) tp[i] = g.tp[i];
+  for (int i = tid; i <= g.n_exp; i += 256) {
+    tp[i] = g.tp[i];
+    so[i] = g.offsets[i];
+  }
   __syncthreads();
   const int total = tp[g.n_exp] * g.n_tiles_n;
   const int KT = 2 * ((g.K + 255) / 256);  // (an even number of steps)
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = kPartFloats;
+  constexpr int AJT = 8, BJ = 8;  // A and weight loads per lane and step
 
   const SplitQueue sq = own_plan(total, KT, 16, 256);
   bool own = true;
+  int claim = 0;
   for (WorkItem w = next_item(g, sq, total, KT, 16, 256, s_slot, own); w.tile >= 0;
-       w = next_item(g, sq, total, KT, 16, 256, s_slot, own)) {
+       w = i8::claimed_item(g, sq, claim, total, KT, 16, 256, s_slot, own)) {
     const int lane = opaque_tid() & 63;  // (lane-derived offsets are formed per tile)
-    TileInfo ti = decode_tile(w.tile, tp, g, BM);
+    TileInfo ti = i8::decode(w.tile, tp, so, g.n_exp, g.n_tiles_n, BM);
     ti.e = __builtin_amdgcn_readfirstlane(ti.e);
     ti.nt = __builtin_amdgcn_readfirstlane(ti.nt);
     ti.row0 = __builtin_amdgcn_readfirstlane(ti.row0);
@@ -102,9 +109,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
         sA1[i] = z;
       }
     }
-    // the scales of the tile's rows and weight rows, for the epilogue (read after the K loop's barriers)
-    s_ws[tid] = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
-    if (tid < ti.mvalid) s_xs[tid] = g.a_scale[g.a_rows ? a_row(g, ti, tid) : ti.row0 + tid];
+    // the scales of the tile's rows and weight rows, for the epilogue
+    const float ws_r = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
+    const int xr = tid < ti.mvalid ? tid : ti.mvalid - 1;
+    const float xs_r = g.a_scale[g.a_rows ? a_row(g, ti, xr) : ti.row0 + xr];
     u32x4* st = wave == 0 ? sA0 : (wave == 1 ? sA1 : (wave == 2 ? sB0 : sB1));  // the epilogue's 32 KB of this wave
     // K pieces always take the 2 x 2 layout (their partial tiles share one shape)
     if (w.piece >= 0 || ti.mvalid > 128) {
@@ -115,6 +123,179 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
       MOE_I8_TILE(2, 2, 0, wave * 64, false)
     } else {
       MOE_I8_TILE(1, 2, 0, wave * 64, false)
+    }
+  }
+}
+
+// ============================================================================ ring of stages
+// Launches of medium size: too few 256 x 256 tiles to occupy the chip, so that a step's loads take
+// longer than its products. Tiles of 128 x 128 (a step is 32 KB, four LDS stages) or 64 x 64 (16 KB,
+// eight stages), filled by direct-to-LDS loads three or seven steps ahead: 96 or 112 KB in flight per
+// CU, against 64 KB two steps ahead in the larger tiles. Waves of 32 x 64; in the 64 x 64 tile KH = 2
+// waves share such a part, each taking half of every step's channels, and meet in the LDS.
+// Every step has one shape, and a tile runs a multiple of the stages' number: loads past its last step
+// read that step again, and its weights count as zeros. (With branches around the loads, or out of
+// the unrolled loop, the compiler waits for every load in flight.)
+constexpr int kRingMinSteps = 14, kRingSlots = 512;
+
+// Loads of step kk into a stage (kmax: gemm_i8_tile.h).
+#define MOE_R4_LOAD(stage, kk)                                                                   \
+  do {                                                                                           \
+    const uint32_t ko_ = MOE_I8_KOFF(kk);                                                        \
+    _Pragma("unroll") for (int j_ = 0; j_ < 2; ++j_) {                                           \
+      dma_to_lds<16>(Ab + (uint32_t)(oa[j_] + ko_), (stage) + j_ * NT + wave * 64);              \
+      dma_to_lds<16>(Be + (uint32_t)(ob[j_] + ko_), (stage) + kB + j_ * NT + wave * 64);         \
+    }                                                                                            \
+  } while (0)
+// Step k on stage c; step k + NS - 1 goes into n, the stage that every wave has left at the barrier.
+// Weights past K or past the tile's last step become zeros before it (kz: the first step with such). Six fragment reads, then products with the loads and the
+// other reads among them.
+#define MOE_R4_STEP(c, n, k)                                                                     \
+  do {                                                                                           \
+    __builtin_amdgcn_s_waitcnt(wait_lgkm0_vm(4 * (NS - 2)));                                     \
+    if ((k) >= kz) {                                                                             \
+      if ((k) >= k1 || (int)(k) * 128 > kmax) {                                                  \
+        (c)[kB + wave * 64 + lane] = u32x4{0u, 0u, 0u, 0u};                                      \
+        (c)[kB + NT + wave * 64 + lane] = u32x4{0u, 0u, 0u, 0u};                                 \
+      }                                                                                          \
+      __builtin_amdgcn_s_waitcnt(wait_lgkm0_vm(4 * (NS - 2)));                                   \
+    }                                                                                            \
+    __builtin_amdgcn_s_barrier();                                                                \
+    __builtin_amdgcn_sched_barrier(0);                                                           \
+    w4::frags<1, 2>(c, (c) + kB, ks0, r0, c0, lane, a0, b0);                                     \
+    w4::frags<1, 2>(c, (c) + kB, ks0 + 1, r0, c0, lane, a1, b1);                                 \
+    MOE_R4_LOAD(n, min((k) + NS - 1, k1 - 1));                                                   \
+    w4::mfmas<1, 2>(acc, a0, b0);                                                                \
+    if (KH == 1) w4::frags<1, 2>(c, (c) + kB, 2, r0, c0, lane, a0, b0);                          \
+    w4::mfmas<1, 2>(acc, a1, b1);                                                                \
+    if (KH == 1) {                                                                               \
+      w4::frags<1, 2>(c, (c) + kB, 3, r0, c0, lane, a1, b1);                                     \
+      w4::mfmas<1, 2>(acc, a0, b0);                                                              \
+      w4::mfmas<1, 2>(acc, a1, b1);                                                              \
+    }                                                                                            \
+    MOE_SGB(0x100, 6);                                                                           \
+    _Pragma("unroll") for (int i_ = 0; i_ < 2; ++i_) {                                           \
+      MOE_SGB(0x008, 1);                                                                         \
+      MOE_SGB(0x010, 1);                                                                         \
+      MOE_SGB(0x008, 1);                                                                         \
+      MOE_SGB(0x010, 1);                                                                         \
+      if (KH == 1) MOE_SGB(0x100, 3);                                                            \
+    }                                                                                            \
+    if (KH == 1) MOE_SGB(0x008, 4);                                                              \
+    __builtin_amdgcn_sched_barrier(0);                                                           \
+  } while (0)
+
+template <int BM, int BN, int KH, bool GLU, bool OUTF32>
+__global__ __launch_bounds__(BM / 32 * (BN / 64) * KH * 64) void k_gemm_i8_ring(GemmArgs g) {
+  constexpr int NWR = BM / 32, NWC = BN / 64, NP = NWR * NWC, NW = NP * KH, NT = NW * 64;
+  constexpr int NS = BM == 64 ? 8 : 4;
+  constexpr int kB = BM * 8, kChunks = (BM + BN) * 8;  // a stage: A, then the weights
+  static_assert(BM * 8 == 2 * NT && BN * 8 == 2 * NT, "two loads of each operand per lane and step");
+  __shared__ u32x4 s0[kChunks];
+  __shared__ u32x4 s1[kChunks];
+  __shared__ u32x4 s2[kChunks];
+  __shared__ u32x4 s3[kChunks];
+  __shared__ u32x4 s4[kChunks];  // (s4 .. s7: NS = 8 only)
+  __shared__ u32x4 s5[kChunks];
+  __shared__ u32x4 s6[kChunks];
+  __shared__ u32x4 s7[kChunks];
+  __shared__ float s_xs[BM];
+  __shared__ f32x4 s_ws4[BN / 4];
+  float* s_ws = reinterpret_cast<float*>(s_ws4);
+  __shared__ int tp[kMaxExperts + 1];
+  __shared__ int so[kMaxExperts + 1];
+  __shared__ int s_slot[1 + kQueues];
+  for (int i = threadIdx.x; i <= g.n_exp; i += NT) {
+    tp[i] = g.tp[i];
+    so[i] = g.offsets[i];
+  }
+  __syncthreads();
+  const int total = tp[g.n_exp] * g.n_tiles_n;
+  const int KT = (g.K + 127) / 128;
+  const SplitQueue sq = own_plan(total, KT, kRingMinSteps, kRingSlots);
+  bool own = true;
+  int claim = 0;
+  for (WorkItem w = next_item(g, sq, total, KT, kRingMinSteps, kRingSlots, s_slot, own); w.tile >= 0;
+       w = i8::claimed_item(g, sq, claim, total, KT, kRingMinSteps, kRingSlots, s_slot, own)) {
+    const int tid = opaque_tid(), lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    TileInfo ti = i8::decode(w.tile, tp, so, g.n_exp, g.n_tiles_n, BM);
+    ti.e = __builtin_amdgcn_readfirstlane(ti.e);
+    ti.nt = __builtin_amdgcn_readfirstlane(ti.nt);
+    ti.row0 = __builtin_amdgcn_readfirstlane(ti.row0);
+    ti.mvalid = __builtin_amdgcn_readfirstlane(ti.mvalid);
+    const int k0 = __builtin_amdgcn_readfirstlane(w.k0), k1 = __builtin_amdgcn_readfirstlane(w.k1);
+    const uint8_t* Ab = a_base(g, ti);
+    const uint8_t* Be = g.B + (size_t)ti.e * g.b_exp;
+    const int ch = dma_chunk(wave * 8 + (lane >> 3), lane) * 16;
+    const int kmax = lane_kmax(g.K, ch);
+    uint32_t oa[2], ob[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = (j * NW + wave) * 8 + (lane >> 3);
+      oa[j] = (uint32_t)a_row(g, ti, r < ti.mvalid ? r : ti.mvalid - 1) * (uint32_t)g.lda + (uint32_t)ch;
+      ob[j] = (uint32_t)weight_row<GLU, BN>(r, ti.nt, g) * (uint32_t)g.ldb + (uint32_t)ch;
+    }
+    const int kz = min(g.K / 128, k1);
+    const int part = wave % NP, kh = wave / NP, ks0 = kh * 2;
+    const int r0 = part / NWC * 32, c0 = part % NWC * 64;
+    const float ws_r = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid < BN ? tid : BN - 1, ti.nt, g)];
+    const int xr = tid < ti.mvalid ? tid : ti.mvalid - 1;
+    const float xs_r = g.a_scale[g.a_rows ? a_row(g, ti, xr) : ti.row0 + xr];
+    i32x16 acc[1][2];
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[0][nb][i] = 0;
+    i32x4 a0[1], b0[2], a1[1], b1[2];
+    MOE_R4_LOAD(s0, k0);
+    MOE_R4_LOAD(s1, min(k0 + 1, k1 - 1));
+    MOE_R4_LOAD(s2, min(k0 + 2, k1 - 1));
+    if constexpr (NS == 8) {
+      MOE_R4_LOAD(s3, min(k0 + 3, k1 - 1));
+      MOE_R4_LOAD(s4, min(k0 + 4, k1 - 1));
+      MOE_R4_LOAD(s5, min(k0 + 5, k1 - 1));
+      MOE_R4_LOAD(s6, min(k0 + 6, k1 - 1));
+    }
+    if (tid < BN) s_ws[tid] = ws_r;
+    if (tid < ti.mvalid) s_xs[tid] = xs_r;
+    if (own && tid == 0) claim = atomicAdd(&g.queue[sq.q], 1);
+    for (int k = k0; k < k1; k += NS) {
+      if constexpr (NS == 4) {
+        MOE_R4_STEP(s0, s3, k);
+        MOE_R4_STEP(s1, s0, k + 1);
+        MOE_R4_STEP(s2, s1, k + 2);
+        MOE_R4_STEP(s3, s2, k + 3);
+      } else {
+        MOE_R4_STEP(s0, s7, k);
+        MOE_R4_STEP(s1, s0, k + 1);
+        MOE_R4_STEP(s2, s1, k + 2);
+        MOE_R4_STEP(s3, s2, k + 3);
+        MOE_R4_STEP(s4, s3, k + 4);
+        MOE_R4_STEP(s5, s4, k + 5);
+        MOE_R4_STEP(s6, s5, k + 6);
+        MOE_R4_STEP(s7, s6, k + 7);
+      }
+    }
+    // (the repeated loads are still in flight, into stages used next)
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0Vm0);
+    __syncthreads();  // (every wave is past the stages)
+    if constexpr (KH == 2) {
+      if (kh == 1) i8::store_partial<1, 2, NP * 64>(reinterpret_cast<float*>(s0), acc, tid - NP * 64);
+      __syncthreads();
+      if (kh == 0) i8::add_partial<1, 2, NP * 64>(reinterpret_cast<const float*>(s0), acc, tid);
+    }
+    bool store = true;
+    if (w.piece >= 0) {
+      if (kh == 0) i8::store_partial<1, 2, NP * 64>(g.part + (size_t)w.slot * (BM * BN), acc, tid);
+      store = split_arrive(&g.split_cnt[w.first], w.S, s_slot);
+      if (store && kh == 0)
+        for (int pc = 0; pc < w.S; ++pc)
+          if (pc != w.piece) i8::add_partial<1, 2, NP * 64>(g.part + (size_t)(w.first + pc) * (BM * BN), acc, tid);
+    }
+    if (store && kh == 0) {
+      u32x4* st = (part < NP / 2 ? s2 : s3) + part % (NP / 2) * 512;  // the epilogue's 8 KB of this wave
+      i8::epilogue<1, 2, GLU, OUTF32, BN>(g, ti, acc, s_xs, s_ws, st, r0, c0, lane);
     }
   }
 }
@@ -132,20 +313,26 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   __shared__ f32x4 s_ws4[BN / 4];
   float* s_ws = reinterpret_cast<float*>(s_ws4);
   __shared__ int tp[kMaxExperts + 1];
+  __shared__ int so[kMaxExperts + 1];
   __shared__ int s_slot[1 + kQueues];
-  for (int i = threadIdx.x; i <= g.n_exp; i += 256) tp[i] = g.tp[i];
+  for (int i = threadIdx.x; i <= g.n_exp; i += 256) {
+    tp[i] = g.tp[i];
+    so[i] = g.offsets[i];
+  }
   __syncthreads();
   const int total = tp[g.n_exp] * g.n_tiles_n;
   const int KT = 2 * ((g.K + 255) / 256);
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = 32 * 256;  // words per partial tile
+  constexpr int AJT = 1, BJ = 8;
   const SplitQueue sq = own_plan(total, KT, 16, 512);
   bool own = true;
+  int claim = 0;
   for (WorkItem w = next_item(g, sq, total, KT, 16, 512, s_slot, own); w.tile >= 0;
-       w = next_item(g, sq, total, KT, 16, 512, s_slot, own)) {
+       w = i8::claimed_item(g, sq, claim, total, KT, 16, 512, s_slot, own)) {
     const int tid = opaque_tid(), lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    TileInfo ti = decode_tile(w.tile, tp, g, BM);
+    TileInfo ti = i8::decode(w.tile, tp, so, g.n_exp, g.n_tiles_n, BM);
     ti.e = __builtin_amdgcn_readfirstlane(ti.e);
     ti.nt = __builtin_amdgcn_readfirstlane(ti.nt);
     ti.row0 = __builtin_amdgcn_readfirstlane(ti.row0);
@@ -179,8 +366,9 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
         sA1[i] = z;
       }
     }
-    s_ws[tid] = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
-    if (tid < ti.mvalid) s_xs[tid] = g.a_scale[g.a_rows ? a_row(g, ti, tid) : ti.row0 + tid];
+    const float ws_r = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
+    const int xr = tid < ti.mvalid ? tid : ti.mvalid - 1;
+    const float xs_r = g.a_scale[g.a_rows ? a_row(g, ti, xr) : ti.row0 + xr];
     u32x4* st = sB0 + wave * 512;  // the epilogue's 8 KB of this wave
     MOE_I8_TILE(1, 2, 0, wave * 64, true)
   }
@@ -380,8 +568,8 @@ static hipError_t launch_few(const char* name, const GemmArgs& g, const int32_t*
 static int round8(int v) { return ((v + 7) / 8) * 8; }
 
 template <class K>
-static hipError_t launch_one(const char* name, K kernel, int grid, const GemmArgs& g, hipStream_t s) {
-  return timed_launch(name, s, [&] { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, g); });
+static hipError_t launch_one(const char* name, K kernel, int grid, int threads, const GemmArgs& g, hipStream_t s) {
+  return timed_launch(name, s, [&] { hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, s, g); });
 }
 
 static hipError_t build_tiles_i8(const int32_t* offsets, int n_exp, int n_rows, int BM, int32_t* tp, hipStream_t s) {
@@ -390,10 +578,57 @@ static hipError_t build_tiles_i8(const int32_t* offsets, int n_exp, int n_rows, 
   });
 }
 
-// 256-row tiles when groups average at least 128 rows and the launch has a tile for every CU, 32-row
-// tiles otherwise (the rule of the bf16 kernels, whose pipeline this is).
-static bool large_tiles(int n_rows, int n_exp, int n_tiles_n, int cus) {
-  return n_rows / n_exp >= 128 && (long)((n_rows + 255) / 256) * n_tiles_n >= cus;
+enum { kTiles256, kTiles128, kTiles64, kTiles32 };
+static constexpr int kTileRows[] = {256, 128, 64, 32}, kTileCols[] = {256, 128, 64, 256};
+
+// Estimated microseconds of a product on tiles of `kind` (not kTiles32): rounds of one tile per CU, each a
+// fixed part and its K steps, or the stream of the weights if that takes longer. The constants are
+// measured (a round of 256 tiles at K = 7168: 103, 30 and 15 us; several rounds of the smaller tiles
+// compete for the L2, half as much again where rows are not whole 128-byte lines), the stream's are what
+// grouped products of 4 to 64 rows per expert reach.
+static double tile_time(int kind, int n_rows, int n_exp, int cols, int K, int cus) {
+  static constexpr double fix[] = {16.0, 5.0, 3.0}, one[] = {1.65, 0.45, 0.21}, more[] = {1.65, 0.6, 0.2};
+  static constexpr double stream[] = {4.2e6, 3.0e6, 3.0e6};  // bytes per us
+  const int bm = kTileRows[kind], active = n_rows < n_exp ? n_rows : n_exp;
+  const double m_tiles = n_exp == 1 ? (n_rows + bm - 1) / bm : n_rows > bm / 2 * active ? (double)n_rows / bm + 0.5 * active : active;
+  const double r = m_tiles * ((cols + kTileCols[kind] - 1) / kTileCols[kind]) / cus;
+  const double rounds = n_exp == 1 || r <= 1 ? ceil(r) : r + 0.3;  // (ragged groups leave no clean last round)
+  const double step = (rounds > 1 ? more : one)[kind] * (K % 128 && kind != kTiles256 ? 1.5 : 1.0);
+  const double t = rounds * (fix[kind] + (K + 127) / 128 * step);
+  const double w = (double)active * cols * K / stream[kind];
+  return t > w ? t : w;
+}
+
+// Tile shape of a call of one or two products (cols2 = 0: one) of the same row groups. Groups of a few
+// rows whose weights fill the chip: 32 x 256 tiles, which keep the most weight bytes in flight
+// (1024 rows over 32 experts of 3600 x 3600: 102 us, the others 115 to 134). Else by estimated time:
+// 4096 x 7168 weights, microseconds with 256 / 128 / 64 / 32-row tiles: 256 rows 93 / 38 / 23 / 48,
+// 1024 rows 107 / 41 / 66 / 63, 2048 rows 119 / 77 / 152 / 142, 8192 rows 215 / 313 / 573 / 457.
+static int tile_kind(int n_rows, int n_exp, int cols, int K, int cols2, int K2, int cus) {
+  const int active = n_rows < n_exp ? n_rows : n_exp;
+  if (n_rows <= 32 * n_exp && (long)active * ((cols + 255) / 256) >= cus) return kTiles32;
+  int best = kTiles256;
+  double t_best = 0;
+  for (int kind = kTiles256; kind <= kTiles64; ++kind) {
+    double t = tile_time(kind, n_rows, n_exp, cols, K, cus);
+    if (cols2) t += tile_time(kind, n_rows, n_exp, cols2, K2, cus);
+    if (kind == kTiles256 || t < t_best) {
+      best = kind;
+      t_best = t;
+    }
+  }
+  return best;
+}
+
+template <bool GLU, bool OUTF32>
+static hipError_t launch_tiles(const char* const (&names)[4], int kind, GemmArgs g, int cus, hipStream_t s) {
+  g.n_tiles_n = ((GLU ? 2 : 1) * g.N_out + kTileCols[kind] - 1) / kTileCols[kind];
+  switch (kind) {
+    case kTiles256: return launch_one(names[kind], k_gemm_i8_w4<GLU, OUTF32>, round8(cus), 256, g, s);
+    case kTiles128: return launch_one(names[kind], k_gemm_i8_ring<128, 128, 1, GLU, OUTF32>, round8(cus), 512, g, s);
+    case kTiles64: return launch_one(names[kind], k_gemm_i8_ring<64, 64, 2, GLU, OUTF32>, round8(cus), 256, g, s);
+    default: return launch_one(names[kind], k_gemm_i8_m32<GLU, OUTF32>, round8(cus * 2), 256, g, s);
+  }
 }
 
 static GemmArgs common_args(int32_t* tiles, float* part, int n_exp) {
@@ -423,18 +658,15 @@ hipError_t launch_int8_gemm(const Int8GemmArgs& a, hipStream_t s) {
   g.ldc = (size_t)a.N * (a.y_f32 ? 4 : 2);
   g.K = a.K;
   g.N_out = g.Nb = a.N;
-  g.n_tiles_n = (a.N + 255) / 256;
   if (a.n_rows <= kFewRows)
     return a.y_f32 ? launch_few<false, true>("gemm_i8_f32out_few", g, a.offsets, a.n_rows, s)
                    : launch_few<false, false>("gemm_i8_few", g, a.offsets, a.n_rows, s);
-  const bool large = large_tiles(a.n_rows, a.n_exp, g.n_tiles_n, cus);
-  hipError_t e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s);
+  const int kind = tile_kind(a.n_rows, a.n_exp, a.N, a.K, 0, 0, cus);
+  hipError_t e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, kTileRows[kind], a.tiles, s);
   if (e != hipSuccess) return e;
-  if (large)
-    return a.y_f32 ? launch_one("gemm_i8_f32out", k_gemm_i8_w4<false, true>, round8(cus), g, s)
-                   : launch_one("gemm_i8", k_gemm_i8_w4<false, false>, round8(cus), g, s);
-  return a.y_f32 ? launch_one("gemm_i8_f32out_m32", k_gemm_i8_m32<false, true>, round8(cus * 2), g, s)
-                 : launch_one("gemm_i8_m32", k_gemm_i8_m32<false, false>, round8(cus * 2), g, s);
+  static const char* const f32[] = {"gemm_i8_f32out", "gemm_i8_f32out_m128", "gemm_i8_f32out_m64", "gemm_i8_f32out_m32"};
+  static const char* const b16[] = {"gemm_i8", "gemm_i8_m128", "gemm_i8_m64", "gemm_i8_m32"};
+  return a.y_f32 ? launch_tiles<false, true>(f32, kind, g, cus, s) : launch_tiles<false, false>(b16, kind, g, cus, s);
 }
 
 hipError_t launch_expert_ffn_int8(const FfnArgs& a, hipStream_t s) {
@@ -457,7 +689,6 @@ hipError_t launch_expert_ffn_int8(const FfnArgs& a, hipStream_t s) {
   g1.K = H;
   g1.N_out = g1.glu_I = I;
   g1.Nb = 2 * I;
-  g1.n_tiles_n = I / 128;
   // Linear-2: [rows, I] x [H, I]^T -> y [rows, H]
   g2.queue += kQueues;
   g2.split_cnt += kMaxSplitItems;
@@ -473,21 +704,21 @@ hipError_t launch_expert_ffn_int8(const FfnArgs& a, hipStream_t s) {
   g2.ldc = (size_t)H * 2;
   g2.K = I;
   g2.N_out = g2.Nb = H;
-  g2.n_tiles_n = (H + 255) / 256;
-  const bool few = a.n_rows <= kFewRows, large = large_tiles(a.n_rows, a.n_exp, g1.n_tiles_n, cus);
-  const int grid = round8(large ? cus : cus * 2);
+  const bool few = a.n_rows <= kFewRows;
+  const int kind = tile_kind(a.n_rows, a.n_exp, 2 * I, H, H, I, cus);
   hipError_t e;
-  if (!few && (e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, large ? 256 : 32, a.tiles, s)) != hipSuccess) return e;
-  e = few     ? launch_few<true, true>("gemm_i8_gateup_swiglu_few", g1, a.offsets, a.n_rows, s)
-      : large ? launch_one("gemm_i8_gateup_swiglu", k_gemm_i8_w4<true, true>, grid, g1, s)
-              : launch_one("gemm_i8_gateup_swiglu_m32", k_gemm_i8_m32<true, true>, grid, g1, s);
+  if (!few && (e = build_tiles_i8(a.offsets, a.n_exp, a.n_rows, kTileRows[kind], a.tiles, s)) != hipSuccess) return e;
+  static const char* const up[] = {"gemm_i8_gateup_swiglu", "gemm_i8_gateup_swiglu_m128", "gemm_i8_gateup_swiglu_m64",
+                                   "gemm_i8_gateup_swiglu_m32"};
+  static const char* const down[] = {"gemm_i8_down", "gemm_i8_down_m128", "gemm_i8_down_m64", "gemm_i8_down_m32"};
+  e = few ? launch_few<true, true>("gemm_i8_gateup_swiglu_few", g1, a.offsets, a.n_rows, s)
+          : launch_tiles<true, true>(up, kind, g1, cus, s);
   if (e != hipSuccess) return e;
   if ((e = launch_quantize_int8("requantize_int8", a.h, true, a.n_rows, a.n_rows, nullptr, 1, I, a.h_codes,
                                 static_cast<float*>(a.h_scale), s)) != hipSuccess)
     return e;
-  if (few) return launch_few<false, false>("gemm_i8_down_few", g2, a.offsets, a.n_rows, s);
-  return large ? launch_one("gemm_i8_down", k_gemm_i8_w4<false, false>, grid, g2, s)
-               : launch_one("gemm_i8_down_m32", k_gemm_i8_m32<false, false>, grid, g2, s);
+  return few ? launch_few<false, false>("gemm_i8_down_few", g2, a.offsets, a.n_rows, s)
+             : launch_tiles<false, false>(down, kind, g2, cus, s);
 }
 
 }  // namespace moe
