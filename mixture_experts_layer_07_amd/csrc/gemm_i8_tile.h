@@ -222,6 +222,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
 }
 }  // namespace i8
 
+// NTW (in scope): weight loads that do not stay in the caches, where they are used once (see the kernels).
 // The loads of the bf16 tiles with the lane's K offset held inside its row (kmax: the last offset at
 // which the lane's chunk is inside, a multiple of 128 or, in rows shorter than the chunk's place,
 // the negative offset that reads the row's first chunk).
@@ -238,7 +239,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
     _Pragma("unroll") for (int j_ = (J0); j_ < (J1); ++j_) {                                     \
       uint32_t o_ = ob[j_];                                                                      \
       asm volatile("" : "+v"(o_));                                                               \
-      R[j_] = *reinterpret_cast<const u32x4*>(Be + (uint32_t)(o_ + ko_));                        \
+      const u32x4* p_ = reinterpret_cast<const u32x4*>(Be + (uint32_t)(o_ + ko_));               \
+      R[j_] = NTW ? __builtin_nontemporal_load(p_) : *p_;                                        \
     }                                                                                            \
   } while (0)
 #define MOE_I8_BDMA(stage, kk)                                                                   \

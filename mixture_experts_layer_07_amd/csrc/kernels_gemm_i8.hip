@@ -70,6 +70,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = kPartFloats;
   constexpr int AJT = 8, BJ = 8;  // A and weight loads per lane and step
+  constexpr bool NTW = false;     // (m-tiles of one expert share their weights in the L2: 5 % slower without)
 
   const SplitQueue sq = own_plan(total, KT, 16, 256);
   bool own = true;
@@ -325,6 +326,9 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = 32 * 256;  // words per partial tile
   constexpr int AJT = 1, BJ = 8;
+  // (few of these groups have a second m-tile: weights that do not displace the token rows in the L2, a
+  // skewed 128-token decode batch of the DeepSeek-V3 shape 930 -> 856 us in Linear-1, 470 -> 438 in Linear-2)
+  constexpr bool NTW = true;
   const SplitQueue sq = own_plan(total, KT, 16, 512);
   bool own = true;
   int claim = 0;
