@@ -393,9 +393,11 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
 // bytes of every row in whole lines through a corner of the LDS that no other wave touches (11.9,
 // 8.7, 8.2 us).
 // TB: blocks of 16 rows whose sums are held; an expert with more rows takes several passes. NW: waves.
-template <bool GLU, bool OUTF32, int TB, int NW>
+// G: blocks of 16 weight rows of a workgroup (GLU: the gate rows and the up rows).
+template <bool GLU, bool OUTF32, int TB, int NW, int G>
 __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32_t* __restrict__ offsets, int n_rows) {
-  constexpr int G = GLU ? 2 : 1, NT = NW * 64;
+  constexpr int NT = NW * 64;
+  static_assert(G <= 2 && (!GLU || G == 2), "one or two blocks");
   static_assert(NW >= 4, "a ballot over 256 experts");
   __shared__ int red[G * TB * 256];
   __shared__ u32x4 sx_rows[NW * TB * 128];  // per wave: 16 TB rows of 128 bytes
@@ -421,11 +423,12 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
     lo = min(max(offsets[e], 0), n_rows);
     hi = min(max(offsets[e + 1], 0), n_rows);
   }
-  const int n0 = blockIdx.x * 16, K = g.K;
+  const int n0 = blockIdx.x * (GLU ? 16 : 16 * G), K = g.K;
   const int lr = lane & 15, lk = (lane >> 4) * 16;
   // this lane's weight row (clamped: columns past N are not stored) and token rows
-  const uint8_t* wp = g.B + (size_t)e * g.b_exp + (size_t)min(n0 + lr, (GLU ? g.glu_I : g.Nb) - 1) * K;
-  const uint8_t* wu = GLU ? wp + (size_t)g.glu_I * K : wp;
+  const uint8_t* we = g.B + (size_t)e * g.b_exp;
+  const uint8_t* wp = we + (size_t)min(n0 + lr, (GLU ? g.glu_I : g.Nb) - 1) * K;
+  const uint8_t* wu = GLU ? wp + (size_t)g.glu_I * K : we + (size_t)min(n0 + 16 + lr, g.Nb - 1) * K;
   for (; lo < hi; lo += 16 * TB) {
     const int rows = min(hi - lo, 16 * TB), nb = (rows + 15) >> 4;
     for (int i = tid; i < G * TB * 256; i += NT) red[i] = 0;
@@ -459,7 +462,7 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
       for (int u = 0; u < 2; ++u) {
         const int kw = k + u * 64 + lk, ko = kw < K ? kw : 0;
         w[0][u] = *reinterpret_cast<const i32x4*>(wp + ko);
-        if (GLU) w[G - 1][u] = *reinterpret_cast<const i32x4*>(wu + ko);
+        if (G == 2) w[G - 1][u] = *reinterpret_cast<const i32x4*>(wu + ko);
       }
 #pragma unroll
       for (int j = 0; j < 2 * TB; ++j)
@@ -502,26 +505,28 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
         for (int i = 0; i < 4; ++i) atomicAdd(&red[(q * TB + t) * 256 + i * 64 + lane], acc[q][t][i]);
     }
     __syncthreads();
-    // thread (t, lane): token 16 t + lane % 16, channels n0 + 4 (lane / 16) .. + 3
-    const int n = n0 + (lane >> 4) * 4;
-    for (int t = wave; t < nb; t += NW) {
-      const int tok = t * 16 + lr;
+    // wave item (q, t): weight block q (GLU: both) of token block t; lane: token 16 t + lane % 16,
+    // channels n .. n + 3
+    for (int i = wave; i < (GLU ? 1 : G) * nb; i += NW) {
+      const int q = i / nb, t = i - q * nb;
+      const int tok = t * 16 + lr, n = n0 + q * 16 + (lane >> 4) * 4;
       if (tok >= rows || n >= g.N_out) continue;
       const float sx = g.a_scale[g.a_rows ? a_row(g, ti, tok) : lo + tok];
       const float* sw = g.b_scale + (size_t)e * g.b_scale_exp;
       const bool vec = (g.N_out & 3) == 0;
+      const int* rt = red + (q * TB + t) * 256 + lane;
       float v[4];
       if constexpr (GLU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float gate = (float)red[t * 256 + i * 64 + lane] * (sx * sw[n + i]);
-          const float up = (float)red[(TB + t) * 256 + i * 64 + lane] * (sx * sw[g.glu_I + n + i]);
-          v[i] = silu_fast(gate) * up;
+        for (int j = 0; j < 4; ++j) {
+          const float gate = (float)rt[j * 64] * (sx * sw[n + j]);
+          const float up = (float)rt[TB * 256 + j * 64] * (sx * sw[g.glu_I + n + j]);
+          v[j] = silu_fast(gate) * up;
         }
       } else {
         const f32x4 sn = i8::channel_scales(sw, n, g.N_out, vec);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)red[t * 256 + i * 64 + lane] * (sx * sn[i]);
+        for (int j = 0; j < 4; ++j) v[j] = (float)rt[j * 64] * (sx * sn[j]);
       }
       uint8_t* row = g.C + (size_t)(lo + tok) * g.ldc;
       if (vec) {
@@ -531,12 +536,12 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
           *reinterpret_cast<uint2*>(row + (size_t)n * 2) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < g.N_out) {
+        for (int j = 0; j < 4; ++j)
+          if (n + j < g.N_out) {
             if constexpr (OUTF32)
-              reinterpret_cast<float*>(row)[n + i] = v[i];
+              reinterpret_cast<float*>(row)[n + j] = v[j];
             else
-              reinterpret_cast<uint16_t*>(row)[n + i] = (uint16_t)bf16x2(v[i], 0.f);
+              reinterpret_cast<uint16_t*>(row)[n + j] = (uint16_t)bf16x2(v[j], 0.f);
           }
       }
     }
@@ -550,23 +555,38 @@ constexpr int kFewRows = 128;
 
 // Row blocks: as many as the rows fill, two where they are spread over experts (64 rows of 64 experts:
 // 340 us with two blocks, 597 with eight). Eight blocks leave one workgroup per CU by their LDS: four
-// waves each where the grid is larger than the chip (128 x 7168 x 2048: 13.8 us, 15.8 with eight
-// waves), eight where it is not (128 x 4096 x 7168: 19.5 us, 29 with four).
-template <bool GLU, bool OUTF32>
-static hipError_t launch_few(const char* name, const GemmArgs& g, const int32_t* offsets, int n_rows, hipStream_t s) {
-  const dim3 grid((g.N_out + 15) / 16, offsets ? (n_rows < g.n_exp ? n_rows : g.n_exp) : 1);
+// waves each where the grid is larger than the chip (128 rows x 7168 x 2048 on 448 workgroups: 13.8 us,
+// 15.8 with eight waves), eight where it is not (128 rows x 4096 x 7168: 19.5 us, 29 with four).
+template <bool GLU, bool OUTF32, int G>
+static hipError_t launch_few_g(const char* name, const GemmArgs& g, const int32_t* offsets, int n_rows, hipStream_t s) {
+  const int cols = GLU ? 16 : 16 * G;
+  const dim3 grid((g.N_out + cols - 1) / cols, offsets ? (n_rows < g.n_exp ? n_rows : g.n_exp) : 1);
   return timed_launch(name, s, [&] {
     if (n_rows <= 16)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 1, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 1, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
     else if (n_rows <= 32 || g.n_exp > 1)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 2, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 2, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
     else if (n_rows <= 64)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 4, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 4, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
     else if ((int)grid.x > dev_info().cus)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 4>), grid, dim3(256), 0, s, g, offsets, n_rows);
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 4, G>), grid, dim3(256), 0, s, g, offsets, n_rows);
     else
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 8>), grid, dim3(512), 0, s, g, offsets, n_rows);
+      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
   });
+}
+template <bool GLU, bool OUTF32>
+static hipError_t launch_few(const char* name, const GemmArgs& g, const int32_t* offsets, int n_rows, hipStream_t s) {
+  if constexpr (GLU) {
+    return launch_few_g<true, OUTF32, 2>(name, g, offsets, n_rows, s);
+  } else {
+    const int active = offsets ? (n_rows < g.n_exp ? n_rows : g.n_exp) : 1;
+    // 32 weight rows per workgroup where that leaves three quarters of the chip or more to work (32 experts
+    // of 7168 x 2048, one row each: 97 us, 122 with 16; 128 rows x 7168 x 2048: 12.1, 13.6), 16 else
+    // (128 rows x 4096 x 7168, 128 workgroups: 19.4 us, 24.6 with 32)
+    if (4 * (long)((g.N_out + 31) / 32) * active >= 3 * dev_info().cus)
+      return launch_few_g<false, OUTF32, 2>(name, g, offsets, n_rows, s);
+    return launch_few_g<false, OUTF32, 1>(name, g, offsets, n_rows, s);
+  }
 }
 
 static int round8(int v) { return ((v + 7) / 8) * 8; }

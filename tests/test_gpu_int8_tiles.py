@@ -22,6 +22,9 @@ TILES = {
     "few-4": ([61], 130, 4000, "_few"),
     "few-8-small-grid": ([127], 1025, 1936, "_few"),
     "few-8-large-grid": ([97], 4130, 528, "_few"),
+    "few-32-weight-rows": ([15], 6161, 1040, "_few"),
+    "few-32-weight-rows-groups": ([1, 0, 35, 2, 0, 17, 16, 1], 1330, 528, "_few"),
+    "few-8-32-weight-rows": ([115], 8290, 272, "_few"),
     "m64": ([140], 770, 400, "_m64"),
     "m64-K-pieces": ([300], 300, 7152, "_m64"),
     "m64-one-step": ([333], 1000, 112, "_m64"),
