@@ -436,6 +436,25 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
     const uint8_t* xb = g.a_rows ? g.A : g.A + (size_t)lo * g.lda;
     TileInfo ti;
     ti.row0 = lo;
+    // epilogue items (q, t): weight block q (GLU: both) of token block t, one per wave and round; lane:
+    // token 16 t + lane % 16, channels n .. n + 3. Their scales are read here, beside the first loads.
+    constexpr int ROUNDS = ((GLU ? 1 : G) * TB + NW - 1) / NW;
+    const bool vec = (g.N_out & 3) == 0;
+    const float* sw = g.b_scale + (size_t)e * g.b_scale_exp;
+    float sx_[ROUNDS];
+    f32x4 sn_[ROUNDS], su_;
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int it = i * NW + wave, q = it / nb, t = it - q * nb;
+      const int tok = min(t * 16 + lr, rows - 1), n = n0 + min(q, G - 1) * 16 + (lane >> 4) * 4;
+      sx_[i] = g.a_scale[g.a_rows ? a_row(g, ti, tok) : lo + tok];
+      if constexpr (GLU) {
+        sn_[i] = *reinterpret_cast<const f32x4*>(sw + n0 + (lane >> 4) * 4);
+        su_ = *reinterpret_cast<const f32x4*>(sw + g.glu_I + n0 + (lane >> 4) * 4);
+      } else {
+        sn_[i] = i8::channel_scales(sw, n, g.N_out, vec);
+      }
+    }
     i32x4 acc[G][TB];
 #pragma unroll
     for (int q = 0; q < G; ++q)
@@ -505,28 +524,17 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
         for (int i = 0; i < 4; ++i) atomicAdd(&red[(q * TB + t) * 256 + i * 64 + lane], acc[q][t][i]);
     }
     __syncthreads();
-    // wave item (q, t): weight block q (GLU: both) of token block t; lane: token 16 t + lane % 16,
-    // channels n .. n + 3
-    for (int i = wave; i < (GLU ? 1 : G) * nb; i += NW) {
-      const int q = i / nb, t = i - q * nb;
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int it = i * NW + wave, q = it / nb, t = it - q * nb;
       const int tok = t * 16 + lr, n = n0 + q * 16 + (lane >> 4) * 4;
-      if (tok >= rows || n >= g.N_out) continue;
-      const float sx = g.a_scale[g.a_rows ? a_row(g, ti, tok) : lo + tok];
-      const float* sw = g.b_scale + (size_t)e * g.b_scale_exp;
-      const bool vec = (g.N_out & 3) == 0;
+      if (it >= (GLU ? 1 : G) * nb || tok >= rows || n >= g.N_out) continue;
       const int* rt = red + (q * TB + t) * 256 + lane;
       float v[4];
-      if constexpr (GLU) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float gate = (float)rt[j * 64] * (sx * sw[n + j]);
-          const float up = (float)rt[TB * 256 + j * 64] * (sx * sw[g.glu_I + n + j]);
-          v[j] = silu_fast(gate) * up;
-        }
-      } else {
-        const f32x4 sn = i8::channel_scales(sw, n, g.N_out, vec);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (float)rt[j * 64] * (sx * sn[j]);
+      for (int j = 0; j < 4; ++j) {
+        v[j] = (float)rt[j * 64] * (sx_[i] * sn_[i][j]);
+        if constexpr (GLU) v[j] = silu_fast(v[j]) * ((float)rt[TB * 256 + j * 64] * (sx_[i] * su_[j]));
       }
       uint8_t* row = g.C + (size_t)(lo + tok) * g.ldc;
       if (vec) {
