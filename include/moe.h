@@ -72,7 +72,8 @@ typedef enum moe_status {
  *               scale per token (see moe_quantize_int8); expert weights are int8 codes with one
  *               fp32 scale per output channel (row); int32 accumulation, exact; the SwiGLU output
  *               is formed in fp32 and re-quantised to int8 with one scale per row; y_perm and
- *               y_shared are bf16, out fp32 or bf16. H, I and I_shared of at most 32768.
+ *               y_shared are bf16, out fp32 or bf16. H, I and I_shared of at most 32768, T*K of
+ *               at most 2^30.
  *
  * MX scale arrays. An operand of R rows and C channels (C a multiple of 128) has its E8M0 scale
  * codes (value 2^(code-127)) stored as [C/128][R][4] bytes: the 4-byte word at (g, r) holds the
@@ -361,7 +362,7 @@ moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* we
  *   y          device [n_rows,N] out, of type y_dtype (MOE_F32 or MOE_BF16)
  *   ws         device workspace of moe_gemm_int8_workspace_size() bytes, one call at a time; needs no
  *              initialisation
- * Any N up to 2^20; K a multiple of 16, at most 131071 (MOE_ERR_UNSUPPORTED otherwise);
+ * n_rows up to 2^30, any N up to 2^20; K a multiple of 16, at most 131071 (MOE_ERR_UNSUPPORTED otherwise);
  * n_experts*N*K is not limited, N*K is below 2^31. x, w, w_scale, y and ws are 16-byte aligned. */
 size_t moe_gemm_int8_workspace_size(void);
 moe_status moe_gemm_int8(int32_t n_experts, int32_t n_rows, int32_t N, int32_t K, const int32_t* offsets, const int8_t* x,

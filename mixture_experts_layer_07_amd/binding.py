@@ -224,11 +224,6 @@ def moe_quantize_mx(rows, cols, inp, codes, scales, stream=None):
            "moe_quantize_mx")
 
 
-def moe_quantize_int8(rows, cols, inp, codes, scales, stream=None):
-    _check(lib().moe_quantize_int8(rows, cols, _p(inp), _p(codes), _p(scales), _stream(stream)),
-           "moe_quantize_int8")
-
-
 def _bad(where, why):
     raise MoEError(1, where, why)
 
@@ -267,6 +262,17 @@ def _here(where, t):
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
         _bad(where, f"tensors must be on the current GPU, got {dev}")
     return dev
+
+
+def moe_quantize_int8(rows, cols, inp, codes, scales, stream=None):
+    """int8 rows (include/moe.h, moe_quantize_int8): inp [rows, cols] bf16, codes [rows, cols] int8, scales [rows] fp32."""
+    where = "moe_quantize_int8"
+    dev = _here(where, inp)
+    ip = _flat(where, "inp", inp, torch.bfloat16, rows * cols, dev)
+    cp = _flat(where, "codes", codes, torch.int8, rows * cols, dev)
+    sp = _flat(where, "scales", scales, torch.float32, rows, dev)
+    if rows:
+        _check(lib().moe_quantize_int8(rows, cols, ip, cp, sp, _stream(stream)), where)
 
 
 def moe_rmsnorm(x, weight, eps, y=None, residual=None, residual_out=None, quant=None, codes=None, scales=None,

@@ -460,6 +460,7 @@ moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* we
   if (c.quant != 0 ? (!codes || !scales) : (codes || scales))
     return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: codes and scales go with quant");
   if (!y && !codes) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: no output (y or codes)");
+  if (y && y == residual_out) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: y and residual_out are one buffer");
   if (reinterpret_cast<uintptr_t>(codes) % 8 || reinterpret_cast<uintptr_t>(scales) % 4)
     return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: codes and scales must be 8- and 4-byte aligned");
   if (c.rows == 0) return MOE_OK;
@@ -501,6 +502,7 @@ moe_status moe_gemm_int8(int32_t n_experts, int32_t n_rows, int32_t N, int32_t K
     return fail(MOE_ERR_INVALID_ARG, "moe_gemm_int8: y_dtype must be MOE_F32 or MOE_BF16");
   if (K % 16) return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: K must be a multiple of 16");
   if (K > kMaxInt8K) return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: K above 131071 could overflow the int32 sums");
+  if (n_rows > (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: n_rows above 2^30 is not supported");
   if ((int64_t)N * K >= (int64_t(1) << 31) || N > (1 << 20))
     return fail(MOE_ERR_UNSUPPORTED, "moe_gemm_int8: N above 2^20 or one expert of 2^31 codes is not supported");
   if (!x || !x_scale || !w || !w_scale || !y || (!offsets && n_experts > 1))

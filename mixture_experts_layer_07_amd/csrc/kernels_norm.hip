@@ -19,6 +19,12 @@
 
 namespace moe {
 
+// Workgroup (x, y) takes row y * kGridRows + x (a grid of one dimension ends at 2^32 threads).
+constexpr int kGridRows = 1 << 16;
+static dim3 row_grid(int rows) {
+  return rows <= kGridRows ? dim3(rows) : dim3(kGridRows, (unsigned)((rows + (int64_t)kGridRows - 1) / kGridRows));
+}
+
 // 8 consecutive channels as fp32. Row strides need not keep rows 16-byte aligned: the vector types
 // carry the element's alignment only, and gfx950 takes unaligned global accesses (the compiler
 // emits one 16-byte load either way).
@@ -195,7 +201,8 @@ template <int V, int Q>
 __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
   __shared__ double red[16];
   __shared__ uint32_t redm[16];
-  const int row = blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
+  const int row = blockIdx.y * kGridRows + blockIdx.x, tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
+  if (row >= a.rows) return;
   const bool xf = a.x_f32, rf = a.r_f32;
   const uint8_t* xr = static_cast<const uint8_t*>(a.x) + (size_t)row * a.x_bytes;
   float s[V][8];
@@ -288,11 +295,12 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
 // Rows to int8, one workgroup per row: scale = absmax / 127, code = rint(v / scale). Destination
 // row i reads source row i, or (index given) row index[i] / div of nsrc, clamped into the source.
 template <int V>
-__global__ __launch_bounds__(1024) void k_quantize_int8(const uint8_t* __restrict__ in, bool f32, int nsrc,
+__global__ __launch_bounds__(1024) void k_quantize_int8(const uint8_t* __restrict__ in, bool f32, int rows, int nsrc,
                                                         const int32_t* __restrict__ index, int div, int cols,
                                                         int8_t* __restrict__ codes, float* __restrict__ scales) {
   __shared__ uint32_t red[16];
-  const int row = blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
+  const int row = blockIdx.y * kGridRows + blockIdx.x, tid = threadIdx.x, nt = blockDim.x;
+  if (row >= rows) return;
   unsigned src = (unsigned)row;
   if (index) {
     src = (unsigned)index[row] / (unsigned)div;
@@ -335,9 +343,9 @@ static hipError_t launch_norm_q(const char* name, const NormArgs& a, hipStream_t
   row_shape(a.cols, &V, &nt);
   return timed_launch(name, s, [&] {
     switch (V) {
-      case 1: hipLaunchKernelGGL((k_rmsnorm<1, Q>), dim3(a.rows), dim3(nt), 0, s, a); break;
-      case 2: hipLaunchKernelGGL((k_rmsnorm<2, Q>), dim3(a.rows), dim3(nt), 0, s, a); break;
-      default: hipLaunchKernelGGL((k_rmsnorm<4, Q>), dim3(a.rows), dim3(nt), 0, s, a);
+      case 1: hipLaunchKernelGGL((k_rmsnorm<1, Q>), row_grid(a.rows), dim3(nt), 0, s, a); break;
+      case 2: hipLaunchKernelGGL((k_rmsnorm<2, Q>), row_grid(a.rows), dim3(nt), 0, s, a); break;
+      default: hipLaunchKernelGGL((k_rmsnorm<4, Q>), row_grid(a.rows), dim3(nt), 0, s, a);
     }
   });
 }
@@ -359,9 +367,9 @@ hipError_t launch_quantize_int8(const char* name, const void* in, bool f32, int 
   int8_t* c = static_cast<int8_t*>(codes);
   return timed_launch(name, s, [&] {
     switch (V) {
-      case 1: hipLaunchKernelGGL(k_quantize_int8<1>, dim3(rows), dim3(nt), 0, s, p, f32, nsrc, index, div, cols, c, scales); break;
-      case 2: hipLaunchKernelGGL(k_quantize_int8<2>, dim3(rows), dim3(nt), 0, s, p, f32, nsrc, index, div, cols, c, scales); break;
-      default: hipLaunchKernelGGL(k_quantize_int8<4>, dim3(rows), dim3(nt), 0, s, p, f32, nsrc, index, div, cols, c, scales);
+      case 1: hipLaunchKernelGGL(k_quantize_int8<1>, row_grid(rows), dim3(nt), 0, s, p, f32, rows, nsrc, index, div, cols, c, scales); break;
+      case 2: hipLaunchKernelGGL(k_quantize_int8<2>, row_grid(rows), dim3(nt), 0, s, p, f32, rows, nsrc, index, div, cols, c, scales); break;
+      default: hipLaunchKernelGGL(k_quantize_int8<4>, row_grid(rows), dim3(nt), 0, s, p, f32, rows, nsrc, index, div, cols, c, scales);
     }
   });
 }

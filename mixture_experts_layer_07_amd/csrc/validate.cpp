@@ -94,6 +94,8 @@ moe_status check_config(const moe_config* c, std::string* why) {
     return bad(MOE_ERR_UNSUPPORTED, "one expert above 2^31 elements is not supported");
   if (c->dtype == MOE_INT8 && (c->H > kMaxRowCols || maxI > kMaxRowCols))
     return bad(MOE_ERR_UNSUPPORTED, "int8 layers need H, I and I_shared of at most 32768");
+  if (c->dtype == MOE_INT8 && P > (int64_t(1) << 30))
+    return bad(MOE_ERR_UNSUPPORTED, "int8 layers need T*K of at most 2^30");
   return MOE_OK;
 }
 

@@ -6,7 +6,8 @@ kernel launch that fills the same buffers (it reads the router weights K-major, 
 at construction).
 With norm_weight given, forward(x, residual) first runs moe_rmsnorm on x + residual (the residual is
 updated in place): its rows feed the router and, quantised in the same pass, the experts of fp8, MX
-and int8 layers.
+and int8 layers. (With gather=False the permuted copy, and in the single launch its own copy, is
+quantised from the rounded rows instead.)
 With gather=True (the default) the permute stage only builds the pair order (and, for fp8, MX and
 int8 layers without a norm, quantises the T input rows once) and Linear-1 of the routed experts reads the token rows in
 place (moe_expert_ffn_gather); with gather=False the permute stage also writes the permuted

@@ -335,3 +335,60 @@ def test_layer_with_norm(dtype):
     layer(x)
     n, _ = orc.rmsnorm(x.double().cpu().numpy(), g.double().cpu().numpy(), 1e-5)
     assert (np.abs(layer.xn.double().cpu().numpy() - n) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(n)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp4"])
+def test_single_launch_layer_with_norm(dtype):
+    """The norm in front of the one-launch decode layer: its output is that of the launch on the normed rows."""
+    cfg = BASE.scaled(T=33, H=768, I=256, E=16, K=4, n_group=4, topk_group=2, I_shared=256, dtype=dtype)
+    g = (1 + 0.1 * torch.randn(cfg.H)).cuda()
+    layer, x, _, _ = layer_of(cfg, fused=True, norm_weight=g)
+    res = torch.randn(cfg.T, cfg.H, device="cuda")            # (an fp32 residual stream)
+    out = layer(x, res).clone()
+    plain, _, _, _ = layer_of(cfg, fused=True)
+    assert torch.equal(plain(layer.xn), out) and layer.device_error() == 0
+    n, _ = orc.rmsnorm(x.double().cpu().numpy(), g.double().cpu().numpy(), 1e-6)
+    layer(x)
+    assert (np.abs(layer.xn.double().cpu().numpy() - n) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(n)).all()
+
+
+def test_two_layers_on_two_streams():
+    """Two int8 layers, each with its buffers and stream, in flight at once give what they give alone."""
+    cfg = LAYERS["dsv3"]
+    a, xa, _, _ = layer_of(cfg)
+    b, xb, _, _ = layer_of(cfg.scaled(T=300, seed=11))
+    wa, wb = a(xa).clone(), b(xb).clone()
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        a.out.zero_()
+        b.out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            with torch.cuda.stream(sa):
+                a(xa)
+            with torch.cuda.stream(sb):
+                b(xb)
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, wa) and torch.equal(b.out, wb)
+
+
+def test_int8_layer_graph_replays():
+    """The whole int8 layer captured, replayed with new inputs and eager work in between."""
+    cfg = LAYERS["decode"]
+    layer, x, _, _ = layer_of(cfg)
+    eager, _, _, _ = layer_of(cfg)
+    xin = x.clone()
+    layer(xin)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(xin)
+    for k in range(4):
+        xin.copy_(x.roll(k, 0) * (1.0 + k))
+        want = eager(xin).clone()
+        layer.out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.out, want), f"replay {k}"

@@ -263,6 +263,28 @@ def test_rmsnorm_streams_and_graph():
         assert torch.equal(yg, y) and torch.equal(rg, ro) and torch.equal(cg, c) and torch.equal(sg, s), f"replay {k}"
 
 
+@pytest.mark.parametrize("rows", [65535, 65536, 65537, 200001])
+def test_many_rows(rows):
+    """Past one dimension of the grid: every row as a call on its own piece gives it."""
+    x = torch.randn((rows, 128), device="cuda").to(torch.bfloat16)
+    g = torch.ones(128, device="cuda")
+    y = torch.full((rows + 1, 128), -7.0, dtype=torch.bfloat16, device="cuda")
+    c, s = codes_for("int8", rows, 128)
+    B.moe_rmsnorm(x, g, 1e-6, y=y[:rows], quant="int8", codes=c[:rows], scales=s)
+    cq, sq = codes_for("int8", rows, 128)
+    B.moe_quantize_int8(rows, 128, x, cq[:rows], sq)
+    torch.cuda.synchronize()
+    assert (y[rows] == -7).all() and (c[rows] == 99).all() and (cq[rows] == 99).all()
+    for lo in range(0, rows, 40000):
+        hi = min(rows, lo + 40000)
+        yp = torch.empty((hi - lo, 128), dtype=torch.bfloat16, device="cuda")
+        cp, sp = codes_for("int8", hi - lo, 128)
+        B.moe_rmsnorm(x[lo:hi], g, 1e-6, y=yp, quant="int8", codes=cp[:hi - lo], scales=sp)
+        assert torch.equal(yp, y[lo:hi]) and torch.equal(cp[:hi - lo], c[lo:hi]) and torch.equal(sp, s[lo:hi])
+        B.moe_quantize_int8(hi - lo, 128, x[lo:hi], cp[:hi - lo], sp)
+        assert torch.equal(cp[:hi - lo], cq[lo:hi]) and torch.equal(sp, sq[lo:hi])
+
+
 def test_rmsnorm_refuses_mixed_tensors():
     x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
     g = torch.ones(128, device="cuda")
