@@ -159,6 +159,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
   const int row0 = __builtin_amdgcn_readfirstlane(ti.row0), mvalid = __builtin_amdgcn_readfirstlane(ti.mvalid);
   const __amdgpu_buffer_rsrc_t rc =
       __builtin_amdgcn_make_buffer_rsrc(g.C + (size_t)row0 * g.ldc, (short)0, mvalid * ldc, 0x00020000);
+  // every column of the tile is one of y's, and y's rows are at least 4-byte aligned
+  const bool whole = GLU || ((ti.nt + 1) * BN <= g.N_out && (F32 || !(g.N_out & 1)));
   auto swz = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
 #pragma unroll
   for (int pass = 0; pass < PASSES; ++pass) {
@@ -199,14 +201,17 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
     const int n = (GLU ? ti.nt * (BN / 2) + c0 / 2 : ti.nt * BN + c0 + pass * COLS) + c * EPC;
     int rbase = lane / CH;
     asm volatile("" : "+v"(rbase));  // (row offsets formed here, not held across the K loop)
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < MB * 32 / RPI; ++i) {
-      const int row = rbase + i * RPI;
-      const u32x4 v = st[row * CH + (c ^ swz(row))];
-      const int off = (r0 + row) * ldc + n * ES;
-      if (GLU || (n + EPC <= g.N_out && (F32 || !(g.N_out & 1)))) {  // (rows are 4-byte aligned)
-        __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, 0);
-      } else {
+      for (int i = 0; i < MB * 32 / RPI; ++i) {
+        const int row = rbase + i * RPI;
+        __builtin_amdgcn_raw_buffer_store_b128(st[row * CH + (c ^ swz(row))], rc, (r0 + row) * ldc + n * ES, 0, 0);
+      }
+    } else {
+      for (int i = 0; i < MB * 32 / RPI; ++i) {
+        const int row = rbase + i * RPI;
+        const u32x4 v = st[row * CH + (c ^ swz(row))];
+        const int off = (r0 + row) * ldc + n * ES;
 #pragma unroll
         for (int k = 0; k < EPC; ++k)
           if (n + k < g.N_out) {
@@ -314,7 +319,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
 #define MOE_I8_TILE(MB_, NB_, r0_, c0_, SPLIT)                                                   \
   {                                                                                              \
     const int r0 = (r0_), c0 = (c0_);                                                            \
-    constexpr int AJ = AJT == 4 ? 4 : ((MB_) * (NB_) == 16 ? 8 : (MB_)); /* A loads per wave, step */ \
+    constexpr int AJ = (NB_) == 4 ? 2 * (MB_) : (MB_); /* A loads per wave, step */                \
     constexpr int L1_ = (BJ * 3 + 7) / 8;                                                        \
     i32x16 acc[MB_][NB_];                                                                        \
     _Pragma("unroll") for (int mb = 0; mb < (MB_); ++mb)                                         \

@@ -44,7 +44,9 @@ __device__ __forceinline__ int lane_kmax(int K, int ch) {
 }
 
 // ============================================================================ 256 x 256 tiles
-// Four waves of 128 x 128 (one per SIMD), shorter layouts for ragged m-tiles, as k_gemm_bf16_w4.
+// Four waves of 128 x 128 (one per SIMD), shorter layouts for ragged m-tiles, as k_gemm_bf16_w4, and
+// one of 96 x 128 for 129 to 192 rows (256 experts of 160 rows, 4096 x 7168 weights: 1660 us, 1842
+// with 128 x 128; 7168 x 2048: 972, 1108).
 template <bool GLU, bool OUTF32>
 __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
   constexpr int BM = 256, BN = 256;
@@ -69,7 +71,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
   const int KT = 2 * ((g.K + 255) / 256);  // (an even number of steps)
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = kPartFloats;
-  constexpr int AJT = 8, BJ = 8;  // A and weight loads per lane and step
+  constexpr int BJ = 8;  // weight loads per lane and step
   constexpr bool NTW = false;     // (m-tiles of one expert share their weights in the L2: 5 % slower without)
 
   const SplitQueue sq = own_plan(total, KT, 16, 256);
@@ -116,8 +118,10 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
     const float xs_r = g.a_scale[g.a_rows ? a_row(g, ti, xr) : ti.row0 + xr];
     u32x4* st = wave == 0 ? sA0 : (wave == 1 ? sA1 : (wave == 2 ? sB0 : sB1));  // the epilogue's 32 KB of this wave
     // K pieces always take the 2 x 2 layout (their partial tiles share one shape)
-    if (w.piece >= 0 || ti.mvalid > 128) {
+    if (w.piece >= 0 || ti.mvalid > 192) {
       MOE_I8_TILE(4, 4, (wave >> 1) * 128, (wave & 1) * 128, true)
+    } else if (ti.mvalid > 128) {
+      MOE_I8_TILE(3, 4, (wave >> 1) * 96, (wave & 1) * 128, false)
     } else if (ti.mvalid > 64) {
       MOE_I8_TILE(4, 2, 0, wave * 64, false)
     } else if (ti.mvalid > 32) {
@@ -325,7 +329,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   const int KT = 2 * ((g.K + 255) / 256);
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = 32 * 256;  // words per partial tile
-  constexpr int AJT = 1, BJ = 8;
+  constexpr int BJ = 8;
   // (few of these groups have a second m-tile: weights that do not displace the token rows in the L2, a
   // skewed 128-token decode batch of the DeepSeek-V3 shape 930 -> 856 us in Linear-1, 470 -> 438 in Linear-2)
   constexpr bool NTW = true;
@@ -617,12 +621,17 @@ static constexpr int kTileRows[] = {256, 128, 64, 32}, kTileCols[] = {256, 128, 
 // fixed part and its K steps, or the stream of the weights if that takes longer. The constants are
 // measured (a round of 256 tiles at K = 7168: 103, 30 and 15 us; several rounds of the smaller tiles
 // compete for the L2, half as much again where rows are not whole 128-byte lines), the stream's are what
-// grouped products of 4 to 64 rows per expert reach.
+// grouped products of 4 to 64 rows per expert reach. extra: the m-tiles that an expert's ragged end adds
+// (short 256-row tiles take less than a whole one): over 130 products of 8 to 64 experts, 64 to 400 rows
+// each on average, balanced to skewed as (e + 1)^-1.2, the choice between the two larger kinds costs
+// 0.7 % on average against the better one each time (3.1 % with 0.5 for both).
 static double tile_time(int kind, int n_rows, int n_exp, int cols, int K, int cus) {
   static constexpr double fix[] = {16.0, 5.0, 3.0}, one[] = {1.65, 0.45, 0.21}, more[] = {1.65, 0.6, 0.2};
+  static constexpr double extra[] = {0.3, 0.7, 0.7};
   static constexpr double stream[] = {4.2e6, 3.0e6, 3.0e6};  // bytes per us
   const int bm = kTileRows[kind], active = n_rows < n_exp ? n_rows : n_exp;
-  const double m_tiles = n_exp == 1 ? (n_rows + bm - 1) / bm : n_rows > bm / 2 * active ? (double)n_rows / bm + 0.5 * active : active;
+  const double ragged = (double)n_rows / bm + extra[kind] * active;
+  const double m_tiles = n_exp == 1 ? (n_rows + bm - 1) / bm : ragged > active ? ragged : active;
   const double r = m_tiles * ((cols + kTileCols[kind] - 1) / kTileCols[kind]) / cus;
   const double rounds = n_exp == 1 || r <= 1 ? ceil(r) : r + 0.3;  // (ragged groups leave no clean last round)
   const double step = (rounds > 1 ? more : one)[kind] * (K % 128 && kind != kTiles256 ? 1.5 : 1.0);

@@ -35,6 +35,8 @@ TILES = {
     "m256": ([5000], 3333, 784, ""),
     "m256-two-steps": ([4090], 4091, 240, ""),
     "m256-groups": ([1030, 0, 257, 900, 1, 31, 33, 65, 129, 1500] * 2, 3001, 1296, ""),
+    "m256-heights": ([1100, 129, 160, 161, 191, 0, 192, 193, 256 + 129, 2 * 256 + 192, 256, 255, 128] * 2, 3333, 2064, ""),
+    "m256-heights-two-steps": ([129, 150, 192, 193, 170, 256] * 6, 4001, 240, ""),
     "m256-K-pieces": ([4900], 4096, 16624, ""),
     "m32": ([1, 0, 40, 31, 7, 33, 20, 96] * 8, 2050, 1296, "_m32"),
     "m32-two-steps": ([3, 18, 32, 65] * 40, 600, 208, "_m32"),
@@ -91,6 +93,7 @@ SWIGLU = {
     "m128": (BASE.scaled(T=1300, H=1152, I=640, E=4, K=2, n_group=1, topk_group=1, I_shared=0), "_m128"),
     "m32": (BASE.scaled(T=100, H=2176, I=1152, E=48, K=8, n_group=1, topk_group=1, I_shared=0), "_m32"),
     "m256": (BASE.scaled(T=3900, H=1920, I=1920, E=5, K=2, n_group=1, topk_group=1, I_shared=0), ""),
+    "m256-heights": (BASE.scaled(T=2640, H=1920, I=1920, E=64, K=4, n_group=1, topk_group=1, I_shared=0), ""),
 }
 
 
