@@ -307,7 +307,11 @@ __global__ __launch_bounds__(BM / 32 * (BN / 64) * KH * 64) void k_gemm_i8_ring(
 
 // ============================================================================ 32 x 256 tiles
 // Decode-sized row groups: 1 x 4 waves of 32 x 64, two workgroups per CU, as k_gemm_bf16_m32.
-template <bool GLU, bool OUTF32>
+// NTW: weight loads that do not stay in the caches. Few of these groups have a second m-tile, and the
+// token rows then stay in the L2 (a skewed 128-token decode batch of the DeepSeek-V3 shape: 930 -> 856 us
+// in Linear-1, 470 -> 438 in Linear-2). Not where rows are not whole 128-byte lines: the line that two
+// steps share is then read twice (1024 rows over 32 experts of 3600 x 3600: 131 us, 159 with NTW).
+template <bool GLU, bool OUTF32, bool NTW>
 __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   constexpr int BM = 32, BN = 256;
   __shared__ u32x4 sA0[m32::kStageA];
@@ -330,9 +334,6 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = 32 * 256;  // words per partial tile
   constexpr int BJ = 8;
-  // (few of these groups have a second m-tile: weights that do not displace the token rows in the L2, a
-  // skewed 128-token decode batch of the DeepSeek-V3 shape 930 -> 856 us in Linear-1, 470 -> 438 in Linear-2)
-  constexpr bool NTW = true;
   const SplitQueue sq = own_plan(total, KT, 16, 512);
   bool own = true;
   int claim = 0;
@@ -617,40 +618,39 @@ static hipError_t build_tiles_i8(const int32_t* offsets, int n_exp, int n_rows, 
 enum { kTiles256, kTiles128, kTiles64, kTiles32 };
 static constexpr int kTileRows[] = {256, 128, 64, 32}, kTileCols[] = {256, 128, 64, 256};
 
-// Estimated microseconds of a product on tiles of `kind` (not kTiles32): rounds of one tile per CU, each a
-// fixed part and its K steps, or the stream of the weights if that takes longer. The constants are
-// measured (a round of 256 tiles at K = 7168: 103, 30 and 15 us; several rounds of the smaller tiles
-// compete for the L2, half as much again where rows are not whole 128-byte lines), the stream's are what
-// grouped products of 4 to 64 rows per expert reach. extra: the m-tiles that an expert's ragged end adds
-// (short 256-row tiles take less than a whole one): over 130 products of 8 to 64 experts, 64 to 400 rows
-// each on average, balanced to skewed as (e + 1)^-1.2, the choice between the two larger kinds costs
-// 0.7 % on average against the better one each time (3.1 % with 0.5 for both).
+// Estimated microseconds of a product on tiles of `kind`: rounds of one tile per workgroup, each a fixed
+// part and the tile's K steps (as many as its loop runs), or the stream of the weights where that takes
+// longer. The host does not know how the rows spread over the experts: `extra` m-tiles per expert stand
+// for ragged ends. The constants are fitted to 1000 products of 129 to 8192 rows, 1 to 64 experts (balanced
+// to skewed as (e + 1)^-1.3), N and K to 7168, each run on all four kinds: the kind so chosen takes 1.4 %
+// more than the best of the four on average (128-row tiles always: 10 %, any other kind always: 37 % or more).
 static double tile_time(int kind, int n_rows, int n_exp, int cols, int K, int cus) {
-  static constexpr double fix[] = {16.0, 5.0, 3.0}, one[] = {1.65, 0.45, 0.21}, more[] = {1.65, 0.6, 0.2};
-  static constexpr double extra[] = {0.3, 0.7, 0.7};
-  static constexpr double stream[] = {4.2e6, 3.0e6, 3.0e6};  // bytes per us
+  static constexpr double first[] = {25.0, 8.0, 8.2, 9.0};     // a single round's fixed part
+  static constexpr double fix[] = {3.3, 4.8, 4.0, 7.6};        // that of each further round
+  static constexpr double step[] = {1.5, 0.58, 0.21, 1.5};     // a K step of 128 bytes
+  static constexpr double part[] = {0.96, 1.2, 1.3, 0.93};     // factor on it where rows are not whole 128-byte lines
+  static constexpr double extra[] = {0.69, 0.51, 1.0, 1.0};
+  static constexpr double stream[] = {5.1e6, 3.9e6, 3.9e6, 5.0e6};  // weight bytes per us
+  static constexpr int multiple[] = {2, 4, 8, 2}, per_cu[] = {1, 1, 1, 2};
   const int bm = kTileRows[kind], active = n_rows < n_exp ? n_rows : n_exp;
   const double ragged = (double)n_rows / bm + extra[kind] * active;
   const double m_tiles = n_exp == 1 ? (n_rows + bm - 1) / bm : ragged > active ? ragged : active;
-  const double r = m_tiles * ((cols + kTileCols[kind] - 1) / kTileCols[kind]) / cus;
+  const double r = m_tiles * ((cols + kTileCols[kind] - 1) / kTileCols[kind]) / (per_cu[kind] * cus);
   const double rounds = n_exp == 1 || r <= 1 ? ceil(r) : r + 0.3;  // (ragged groups leave no clean last round)
-  const double step = (rounds > 1 ? more : one)[kind] * (K % 128 && kind != kTiles256 ? 1.5 : 1.0);
-  const double t = rounds * (fix[kind] + (K + 127) / 128 * step);
-  const double w = (double)active * cols * K / stream[kind];
+  const int bytes = 128 * multiple[kind];
+  const int steps = (K + bytes - 1) / bytes * multiple[kind];
+  const double t = first[kind] - fix[kind] + rounds * (fix[kind] + steps * step[kind] * (K % 128 ? part[kind] : 1.0));
+  const double w = first[kind] + (double)active * cols * K / stream[kind];
   return t > w ? t : w;
 }
 
-// Tile shape of a call of one or two products (cols2 = 0: one) of the same row groups. Groups of a few
-// rows whose weights fill the chip: 32 x 256 tiles, which keep the most weight bytes in flight
-// (1024 rows over 32 experts of 3600 x 3600: 102 us, the others 115 to 134). Else by estimated time:
+// Tile shape of a call of one or two products (cols2 = 0: one) of the same row groups, by estimated time.
 // 4096 x 7168 weights, microseconds with 256 / 128 / 64 / 32-row tiles: 256 rows 93 / 38 / 23 / 48,
 // 1024 rows 107 / 41 / 66 / 63, 2048 rows 119 / 77 / 152 / 142, 8192 rows 215 / 313 / 573 / 457.
 static int tile_kind(int n_rows, int n_exp, int cols, int K, int cols2, int K2, int cus) {
-  const int active = n_rows < n_exp ? n_rows : n_exp;
-  if (n_rows <= 32 * n_exp && (long)active * ((cols + 255) / 256) >= cus) return kTiles32;
   int best = kTiles256;
   double t_best = 0;
-  for (int kind = kTiles256; kind <= kTiles64; ++kind) {
+  for (int kind = kTiles256; kind <= kTiles32; ++kind) {
     double t = tile_time(kind, n_rows, n_exp, cols, K, cus);
     if (cols2) t += tile_time(kind, n_rows, n_exp, cols2, K2, cus);
     if (kind == kTiles256 || t < t_best) {
@@ -668,7 +668,9 @@ static hipError_t launch_tiles(const char* const (&names)[4], int kind, GemmArgs
     case kTiles256: return launch_one(names[kind], k_gemm_i8_w4<GLU, OUTF32>, round8(cus), 256, g, s);
     case kTiles128: return launch_one(names[kind], k_gemm_i8_ring<128, 128, 1, GLU, OUTF32>, round8(cus), 512, g, s);
     case kTiles64: return launch_one(names[kind], k_gemm_i8_ring<64, 64, 2, GLU, OUTF32>, round8(cus), 256, g, s);
-    default: return launch_one(names[kind], k_gemm_i8_m32<GLU, OUTF32>, round8(cus * 2), 256, g, s);
+    default:
+      return g.K % 128 ? launch_one(names[kind], k_gemm_i8_m32<GLU, OUTF32, false>, round8(cus * 2), 256, g, s)
+                       : launch_one(names[kind], k_gemm_i8_m32<GLU, OUTF32, true>, round8(cus * 2), 256, g, s);
   }
 }
 
