@@ -112,13 +112,16 @@ __device__ __forceinline__ void add_partial(const float* part, i32x16 (&acc)[MB]
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int n0 = 0; n0 < NB; n0 += 2) {
+      i32x4 v[8];  // eight loads in flight
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const i32x4 v = reinterpret_cast<const i32x4*>(part)[((mb * NB + nb) * 4 + c) * NT + tid];
+      for (int c = 0; c < 8; ++c) v[c] = reinterpret_cast<const i32x4*>(part)[((mb * NB + n0) * 4 + c) * NT + tid];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mb][nb][4 * c + e] += v[e];
-      }
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mb][n0 + c / 4][4 * (c & 3) + e] += v[c][e];
+    }
 }
 
 // Scales of the four consecutive channels n .. n + 3 of an expert of Nb channels (clamped; the
@@ -129,6 +132,20 @@ __device__ __forceinline__ f32x4 channel_scales(const float* sw, int n, int Nb, 
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = sw[n + j < Nb ? n + j : Nb - 1];
   return v;
+}
+
+// Tile rows r (each below mvalid) -> rows of A from a_base: a_row with all the index loads in flight at once.
+template <int N>
+__device__ __forceinline__ void source_rows(const GemmArgs& g, const TileInfo& ti, int (&r)[N]) {
+  if (!g.a_rows) return;
+  unsigned v[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = (unsigned)g.a_rows[ti.row0 + r[j]];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    v[j] /= (unsigned)g.a_div;
+    r[j] = v[j] < (unsigned)g.a_limit ? (int)v[j] : g.a_limit - 1;
+  }
 }
 
 // Epilogue of a wave's MB x NB blocks at rows r0.., weight rows c0.. of the BN-row weight tile. In a
@@ -162,32 +179,42 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
   // every column of the tile is one of y's, and y's rows are at least 4-byte aligned
   const bool whole = GLU || ((ti.nt + 1) * BN <= g.N_out && (F32 || !(g.N_out & 1)));
   auto swz = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
+  constexpr int QN = GLU ? NB / 2 : NBP;
 #pragma unroll
   for (int pass = 0; pass < PASSES; ++pass) {
+    // all the channel scales of the lane first: read at their use, each read is waited for alone
+    f32x4 sn[QN][4], su[GLU ? QN : 1][4];
+#pragma unroll
+    for (int q = 0; q < QN; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = c0 + (GLU ? q * 64 : (pass * NBP + q) * 32) + j * 8 + lk * 4;
+        sn[q][j] = *reinterpret_cast<const f32x4*>(s_ws + at);
+        if constexpr (GLU) su[q][j] = *reinterpret_cast<const f32x4*>(s_ws + at + 32);
+      }
+    float sx[MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) sx[mb] = s_xs[r0 + mb * 32 + lrow];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
       const int row = mb * 32 + lrow;
-      const float sx = s_xs[r0 + row];
       u32x4* dst = st + row * CH;
       const int sw = swz(row);
 #pragma unroll
-      for (int q = 0; q < (GLU ? NB / 2 : NBP); ++q)
+      for (int q = 0; q < QN; ++q)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float v[4];
           if constexpr (GLU) {
-            const f32x4 sg = *reinterpret_cast<const f32x4*>(s_ws + c0 + q * 64 + j * 8 + lk * 4);
-            const f32x4 su = *reinterpret_cast<const f32x4*>(s_ws + c0 + q * 64 + 32 + j * 8 + lk * 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float gate = (float)acc[mb][2 * q][4 * j + i] * (sx * sg[i]);
-              v[i] = silu_fast(gate) * ((float)acc[mb][2 * q + 1][4 * j + i] * (sx * su[i]));
+              const float gate = (float)acc[mb][2 * q][4 * j + i] * (sx[mb] * sn[q][j][i]);
+              v[i] = silu_fast(gate) * ((float)acc[mb][2 * q + 1][4 * j + i] * (sx[mb] * su[q][j][i]));
             }
           } else {
-            const int nb = pass * NBP + q;
-            const f32x4 sn = *reinterpret_cast<const f32x4*>(s_ws + c0 + nb * 32 + j * 8 + lk * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (float)acc[mb][nb][4 * j + i] * (sx * sn[i]);
+            for (int i = 0; i < 4; ++i) v[i] = (float)acc[mb][pass * NBP + q][4 * j + i] * (sx[mb] * sn[q][j][i]);
           }
           if constexpr (F32)
             dst[(q * 8 + j * 2 + lk) ^ sw] =
@@ -202,10 +229,19 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, const TileInfo& ti, 
     int rbase = lane / CH;
     asm volatile("" : "+v"(rbase));  // (row offsets formed here, not held across the K loop)
     if (whole) {
+      constexpr int U = MB * 32 / RPI < 8 ? MB * 32 / RPI : 8;  // reads in flight
 #pragma unroll
-      for (int i = 0; i < MB * 32 / RPI; ++i) {
-        const int row = rbase + i * RPI;
-        __builtin_amdgcn_raw_buffer_store_b128(st[row * CH + (c ^ swz(row))], rc, (r0 + row) * ldc + n * ES, 0, 0);
+      for (int i0 = 0; i0 < MB * 32 / RPI; i0 += U) {
+        u32x4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int row = rbase + (i0 + i) * RPI;
+          v[i] = st[row * CH + (c ^ swz(row))];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          __builtin_amdgcn_raw_buffer_store_b128(v[i], rc, (r0 + rbase + (i0 + i) * RPI) * ldc + n * ES, 0, 0);
       }
     } else {
       for (int i = 0; i < MB * 32 / RPI; ++i) {

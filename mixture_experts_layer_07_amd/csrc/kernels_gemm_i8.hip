@@ -95,12 +95,16 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
     // (the swizzle gives a lane the same chunk in all its rows: they are 32 apart)
     const int ch = dma_chunk(wave * 8 + (lane >> 3), lane) * 16;
     const int kmax = lane_kmax(g.K, ch);
+    int src[9];  // rows of A of this lane's eight loads, and of the token whose scale it reads
+#pragma unroll
+    for (int j = 0; j < 8; ++j) src[j] = min((j * 4 + wave) * 8 + (lane >> 3), ti.mvalid - 1);
+    src[8] = min(tid, ti.mvalid - 1);
+    i8::source_rows(g, ti, src);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int r = (j * 4 + wave) * 8 + (lane >> 3);
       const bool live = (j * 4 + wave) * 8 < arows;  // wave-uniform
-      const int rr = live ? a_row(g, ti, r < ti.mvalid ? r : ti.mvalid - 1) : 0;
-      oa[j] = (uint32_t)rr * (uint32_t)g.lda + (uint32_t)ch;
+      oa[j] = (uint32_t)src[j] * (uint32_t)g.lda + (uint32_t)ch;
       la_off[j] = live ? (j * 4 + wave) * 64 : w4::kSink;
       ob[j] = (uint32_t)weight_row<GLU, BN>(r, ti.nt, g) * (uint32_t)g.ldb + (uint32_t)ch;
     }
@@ -114,8 +118,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
     }
     // the scales of the tile's rows and weight rows, for the epilogue
     const float ws_r = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid, ti.nt, g)];
-    const int xr = tid < ti.mvalid ? tid : ti.mvalid - 1;
-    const float xs_r = g.a_scale[g.a_rows ? a_row(g, ti, xr) : ti.row0 + xr];
+    const float xs_r = g.a_scale[g.a_rows ? src[8] : ti.row0 + src[8]];
     u32x4* st = wave == 0 ? sA0 : (wave == 1 ? sA1 : (wave == 2 ? sB0 : sB1));  // the epilogue's 32 KB of this wave
     // K pieces always take the 2 x 2 layout (their partial tiles share one shape)
     if (w.piece >= 0 || ti.mvalid > 192) {
@@ -235,18 +238,22 @@ __global__ __launch_bounds__(BM / 32 * (BN / 64) * KH * 64) void k_gemm_i8_ring(
     const int ch = dma_chunk(wave * 8 + (lane >> 3), lane) * 16;
     const int kmax = lane_kmax(g.K, ch);
     uint32_t oa[2], ob[2];
+    int src[3];  // rows of A of this lane's two loads, and of the token whose scale it reads
+#pragma unroll
+    for (int j = 0; j < 2; ++j) src[j] = min((j * NW + wave) * 8 + (lane >> 3), ti.mvalid - 1);
+    src[2] = min(tid, ti.mvalid - 1);
+    i8::source_rows(g, ti, src);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = (j * NW + wave) * 8 + (lane >> 3);
-      oa[j] = (uint32_t)a_row(g, ti, r < ti.mvalid ? r : ti.mvalid - 1) * (uint32_t)g.lda + (uint32_t)ch;
+      oa[j] = (uint32_t)src[j] * (uint32_t)g.lda + (uint32_t)ch;
       ob[j] = (uint32_t)weight_row<GLU, BN>(r, ti.nt, g) * (uint32_t)g.ldb + (uint32_t)ch;
     }
     const int kz = min(g.K / 128, k1);
     const int part = wave % NP, kh = wave / NP, ks0 = kh * 2;
     const int r0 = part / NWC * 32, c0 = part % NWC * 64;
     const float ws_r = g.b_scale[(size_t)ti.e * g.b_scale_exp + weight_row<GLU, BN>(tid < BN ? tid : BN - 1, ti.nt, g)];
-    const int xr = tid < ti.mvalid ? tid : ti.mvalid - 1;
-    const float xs_r = g.a_scale[g.a_rows ? a_row(g, ti, xr) : ti.row0 + xr];
+    const float xs_r = g.a_scale[g.a_rows ? src[2] : ti.row0 + src[2]];
     i32x16 acc[1][2];
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb)
