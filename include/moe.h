@@ -345,7 +345,8 @@ typedef struct moe_norm_config {
  *   scales       quant != 0: out, MOE_FP8_E4M3 device [rows,cols/128] fp32, MOE_MXFP4 device MX
  *                scale array of `rows` rows (the code 255, NaN, for a block that holds a NaN or
  *                an infinity), MOE_INT8 device [rows] fp32; else NULL
- * Outputs overlap nothing else. The sum of squares is fp32: |s| up to 1.8e19 / sqrt(cols). eps = 0
+ * Outputs overlap nothing else (an output at the address of an input of another type or stride is
+ * refused). The sum of squares is fp32: |s| up to 1.8e19 / sqrt(cols). eps = 0
  * on an all-zero row gives NaN, as the formula does. */
 moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* weight, const void* residual,
                        void* residual_out, void* y, void* codes, void* scales, void* stream);

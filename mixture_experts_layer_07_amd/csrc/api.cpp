@@ -463,6 +463,17 @@ moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* we
   if (y && y == residual_out) return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: y and residual_out are one buffer");
   if (reinterpret_cast<uintptr_t>(codes) % 8 || reinterpret_cast<uintptr_t>(scales) % 4)
     return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: codes and scales must be 8- and 4-byte aligned");
+  auto bytes = [&](int64_t stride, int32_t dtype) { return (stride ? stride : c.cols) * (dtype == MOE_F32 ? 4 : 2); };
+  // an output in place of an input: each thread then writes what it alone has read
+  struct Rows {
+    const void* p;
+    int32_t dtype;
+    int64_t stride;
+  };
+  for (const Rows& o : {Rows{residual_out, c.residual_dtype, c.residual_out_stride}, Rows{y, c.y_dtype, c.y_stride}})
+    for (const Rows& i : {Rows{x, c.x_dtype, c.x_stride}, Rows{residual, c.residual_dtype, c.residual_stride}})
+      if (o.p && o.p == i.p && (o.dtype != i.dtype || (c.rows > 1 && bytes(o.stride, o.dtype) != bytes(i.stride, i.dtype))))
+        return fail(MOE_ERR_INVALID_ARG, "moe_rmsnorm: an output in place of an input needs its type and stride");
   if (c.rows == 0) return MOE_OK;
   MOE_TRY(ensure_device());
   NormArgs a;
@@ -473,7 +484,6 @@ moe_status moe_rmsnorm(const moe_norm_config* cfg, const void* x, const void* we
   a.y = y;
   a.codes = codes;
   a.scales = scales;
-  auto bytes = [&](int64_t stride, int32_t dtype) { return (stride ? stride : c.cols) * (dtype == MOE_F32 ? 4 : 2); };
   a.x_bytes = bytes(c.x_stride, c.x_dtype);
   a.r_bytes = bytes(c.residual_stride, c.residual_dtype);
   a.ro_bytes = bytes(c.residual_out_stride, c.residual_dtype);

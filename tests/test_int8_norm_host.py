@@ -89,6 +89,13 @@ def test_rmsnorm_refusals(lib):
     assert call(norm_cfg(), y=None) == INVALID                      # nothing to write
     assert call(norm_cfg(), codes=FAKE, scales=FAKE) == INVALID     # codes without quant
     assert call(norm_cfg(), ro=ODD, y=ODD) == INVALID               # two outputs in one buffer
+    # an output in place of an input whose rows lie elsewhere or differ in type
+    for kw in (dict(x_dtype=0), dict(x_stride=512), dict(y_stride=260)):
+        assert call(norm_cfg(**kw), x=OTHER) == INVALID, kw
+        assert call(norm_cfg(rows=0, **kw), x=OTHER) == (INVALID if "x_dtype" in kw else OK), kw
+    assert call(norm_cfg(rows=0, residual_stride=512), r=FAKE, ro=FAKE) == OK
+    assert call(norm_cfg(residual_stride=512), r=FAKE, ro=FAKE) == INVALID
+    assert call(norm_cfg(x_dtype=0, residual_dtype=1), x=FAKE, r=OTHER, ro=FAKE, y=ODD) == INVALID
     for q in (2, 3, 4):
         assert call(norm_cfg(quant=q)) == INVALID
         assert call(norm_cfg(quant=q), codes=FAKE) == INVALID
