@@ -574,24 +574,32 @@ __global__ __launch_bounds__(NW * 64) void k_gemm_i8_few(GemmArgs g, const int32
 constexpr int kFewRows = 128;
 
 // Row blocks: as many as the rows fill, two where they are spread over experts (64 rows of 64 experts:
-// 340 us with two blocks, 597 with eight). Eight blocks leave one workgroup per CU by their LDS: four
-// waves each where the grid is larger than the chip (128 rows x 7168 x 2048 on 448 workgroups: 13.8 us,
-// 15.8 with eight waves), eight where it is not (128 rows x 4096 x 7168: 19.5 us, 29 with four).
+// 340 us with two blocks, 597 with eight).
+// Waves: eight, or four where that keeps more workgroups resident without leaving the chip idle. With
+// one or two row blocks (at most 20 waves per CU by registers: two workgroups of eight or five of four) in
+// rows of at most 2048 channels, where eight waves run one or two steps each (8 experts of 7168 x 2048,
+// one row each: 25.2 us, 29.0 with eight; of 14336 x 1024: 24.9, 33.1), and in grids of one to two workgroups per
+// CU (4 experts of 4096 x 7168: 24.1, 26.3), but not in larger or smaller ones (8 of 4096 x 7168: 45.8, 44.7;
+// one: 12.6, 9.4). With more row blocks in grids larger than the chip (64 rows x 14336 x 2048:
+// 12.4, 14.4; 128 rows x 7168 x 2048 on 448 workgroups: 13.8, 15.8), not in smaller ones (64 rows x
+// 4096 x 7168: 20.3, 16.1; 128 rows: 29, 19.5).
 template <bool GLU, bool OUTF32, int G>
 static hipError_t launch_few_g(const char* name, const GemmArgs& g, const int32_t* offsets, int n_rows, hipStream_t s) {
-  const int cols = GLU ? 16 : 16 * G;
+  const int cols = GLU ? 16 : 16 * G, cus = dev_info().cus;
   const dim3 grid((g.N_out + cols - 1) / cols, offsets ? (n_rows < g.n_exp ? n_rows : g.n_exp) : 1);
+  const long wgs = (long)grid.x * grid.y;
+  const int tb = n_rows <= 16 ? 1 : (n_rows <= 32 || g.n_exp > 1 ? 2 : (n_rows <= 64 ? 4 : 8));
+  const bool four = tb <= 2 ? g.K <= 2048 || (wgs > cus && wgs <= 2 * cus) : wgs > cus;
+  auto go = [&](auto kernel, int waves) {
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, s, g, offsets, n_rows);
+  };
   return timed_launch(name, s, [&] {
-    if (n_rows <= 16)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 1, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
-    else if (n_rows <= 32 || g.n_exp > 1)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 2, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
-    else if (n_rows <= 64)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 4, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
-    else if ((int)grid.x > dev_info().cus)
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 4, G>), grid, dim3(256), 0, s, g, offsets, n_rows);
-    else
-      hipLaunchKernelGGL((k_gemm_i8_few<GLU, OUTF32, 8, 8, G>), grid, dim3(512), 0, s, g, offsets, n_rows);
+    switch (tb) {
+      case 1: four ? go(k_gemm_i8_few<GLU, OUTF32, 1, 4, G>, 4) : go(k_gemm_i8_few<GLU, OUTF32, 1, 8, G>, 8); break;
+      case 2: four ? go(k_gemm_i8_few<GLU, OUTF32, 2, 4, G>, 4) : go(k_gemm_i8_few<GLU, OUTF32, 2, 8, G>, 8); break;
+      case 4: four ? go(k_gemm_i8_few<GLU, OUTF32, 4, 4, G>, 4) : go(k_gemm_i8_few<GLU, OUTF32, 4, 8, G>, 8); break;
+      default: four ? go(k_gemm_i8_few<GLU, OUTF32, 8, 4, G>, 4) : go(k_gemm_i8_few<GLU, OUTF32, 8, 8, G>, 8);
+    }
   });
 }
 template <bool GLU, bool OUTF32>

@@ -25,6 +25,13 @@ TILES = {
     "few-32-weight-rows": ([15], 6161, 1040, "_few"),
     "few-32-weight-rows-groups": ([1, 0, 35, 2, 0, 17, 16, 1], 1330, 528, "_few"),
     "few-8-32-weight-rows": ([115], 8290, 272, "_few"),
+    "few-1-long": ([9], 1030, 4112, "_few"),
+    "few-1-long-32-weight-rows": ([5], 6501, 2064, "_few"),
+    "few-1-two-per-cu": ([3], 5121, 2320, "_few"),
+    "few-2-long-groups": ([2, 0, 17, 9, 1, 30] * 2, 3101, 2064, "_few"),
+    "few-4-large-grid": ([50], 4130, 400, "_few"),
+    "few-4-large-grid-32-weight-rows": ([61], 8301, 528, "_few"),
+    "few-8-small-grid-32-weight-rows": ([99], 7001, 528, "_few"),
     "m64": ([140], 770, 400, "_m64"),
     "m64-K-pieces": ([300], 300, 7152, "_m64"),
     "m64-one-step": ([333], 1000, 112, "_m64"),
@@ -89,6 +96,8 @@ BASE = INT8_CONFIGS[9]
 # the SwiGLU epilogue and the gathered rows on each tile shape: (layer, suffix)
 SWIGLU = {
     "few": (BASE.scaled(T=12, H=640, I=384, E=12, K=5, n_group=1, topk_group=1, I_shared=0), "_few"),
+    "few-long": (BASE.scaled(T=3, H=2176, I=128, E=12, K=5, n_group=1, topk_group=1, I_shared=0), "_few"),
+    "few-long-groups": (BASE.scaled(T=12, H=2176, I=2304, E=12, K=5, n_group=1, topk_group=1, I_shared=0), "_few"),
     "m64": (BASE.scaled(T=60, H=896, I=384, E=8, K=4, n_group=1, topk_group=1, I_shared=0), "_m64"),
     "m128": (BASE.scaled(T=1300, H=1152, I=640, E=4, K=2, n_group=1, topk_group=1, I_shared=0), "_m128"),
     "m32": (BASE.scaled(T=100, H=2176, I=1152, E=48, K=8, n_group=1, topk_group=1, I_shared=0), "_m32"),
