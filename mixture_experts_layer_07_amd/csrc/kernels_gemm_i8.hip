@@ -43,6 +43,16 @@ __device__ __forceinline__ int lane_kmax(int K, int ch) {
   return last >= 0 ? (last & ~127) : -ch;
 }
 
+// Steps of a K piece at least, for `total` tiles on gridDim.x workgroups. Pieces meet at a cost of some 10 us
+// (each publishes its sums past its XCD's L2, the last one reads them all), so tiles are cut where there are next
+// to none of them (64 x 64 tiles: 140 x 512 x 7168 17.1 us in four pieces, 18.6 whole; 256 x 256: 4 x 250 rows x
+// 4096 x 7168 72 us, 80 whole) or where they are very long, and not where they leave half of the chip idle
+// (64 x 64: 256 x 2048 x 7168 19.3 us whole, 27.2 in two pieces; 32 x 256: 300 rows over 16 experts x 4096 x 7168
+// 79 us, 109; 256 x 256: 200 rows over 8 experts 60 us, 90).
+__device__ __forceinline__ int piece_steps(int total, int few, int long_) {
+  return few * total <= (int)gridDim.x ? 14 : long_;
+}
+
 // ============================================================================ 256 x 256 tiles
 // Four waves of 128 x 128 (one per SIMD), shorter layouts for ragged m-tiles, as k_gemm_bf16_w4, and
 // one of 96 x 128 for 129 to 192 rows (256 experts of 160 rows, 4096 x 7168 weights: 1660 us, 1842
@@ -74,11 +84,13 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
   constexpr int BJ = 8;  // weight loads per lane and step
   constexpr bool NTW = false;     // (m-tiles of one expert share their weights in the L2: 5 % slower without)
 
-  const SplitQueue sq = own_plan(total, KT, 16, 256);
+  // (after a full round the plan cuts the rest of the tiles if KT is 128 or more)
+  const int min_steps = total >= (int)gridDim.x ? 16 : piece_steps(total, 4, 64);
+  const SplitQueue sq = own_plan(total, KT, min_steps, 256);
   bool own = true;
   int claim = 0;
-  for (WorkItem w = next_item(g, sq, total, KT, 16, 256, s_slot, own); w.tile >= 0;
-       w = i8::claimed_item(g, sq, claim, total, KT, 16, 256, s_slot, own)) {
+  for (WorkItem w = next_item(g, sq, total, KT, min_steps, 256, s_slot, own); w.tile >= 0;
+       w = i8::claimed_item(g, sq, claim, total, KT, min_steps, 256, s_slot, own)) {
     const int lane = opaque_tid() & 63;  // (lane-derived offsets are formed per tile)
     TileInfo ti = i8::decode(w.tile, tp, so, g.n_exp, g.n_tiles_n, BM);
     ti.e = __builtin_amdgcn_readfirstlane(ti.e);
@@ -144,7 +156,7 @@ __global__ __launch_bounds__(256, 1) void k_gemm_i8_w4(GemmArgs g) {
 // Every step has one shape, and a tile runs a multiple of the stages' number: loads past its last step
 // read that step again, and its weights count as zeros. (With branches around the loads, or out of
 // the unrolled loop, the compiler waits for every load in flight.)
-constexpr int kRingMinSteps = 14, kRingSlots = 512;
+constexpr int kRingSlots = 512;
 
 // Loads of step kk into a stage (kmax: gemm_i8_tile.h).
 #define MOE_R4_LOAD(stage, kk)                                                                   \
@@ -220,11 +232,12 @@ __global__ __launch_bounds__(BM / 32 * (BN / 64) * KH * 64) void k_gemm_i8_ring(
   __syncthreads();
   const int total = tp[g.n_exp] * g.n_tiles_n;
   const int KT = (g.K + 127) / 128;
-  const SplitQueue sq = own_plan(total, KT, kRingMinSteps, kRingSlots);
+  const int min_steps = piece_steps(total, 8, 56);
+  const SplitQueue sq = own_plan(total, KT, min_steps, kRingSlots);
   bool own = true;
   int claim = 0;
-  for (WorkItem w = next_item(g, sq, total, KT, kRingMinSteps, kRingSlots, s_slot, own); w.tile >= 0;
-       w = i8::claimed_item(g, sq, claim, total, KT, kRingMinSteps, kRingSlots, s_slot, own)) {
+  for (WorkItem w = next_item(g, sq, total, KT, min_steps, kRingSlots, s_slot, own); w.tile >= 0;
+       w = i8::claimed_item(g, sq, claim, total, KT, min_steps, kRingSlots, s_slot, own)) {
     const int tid = opaque_tid(), lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     TileInfo ti = i8::decode(w.tile, tp, so, g.n_exp, g.n_tiles_n, BM);
@@ -341,11 +354,12 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8_m32(GemmArgs g) {
   const int kfull = g.K / 128;
   constexpr size_t kPartStride = 32 * 256;  // words per partial tile
   constexpr int BJ = 8;
-  const SplitQueue sq = own_plan(total, KT, 16, 512);
+  const int min_steps = piece_steps(total, 8, 56);
+  const SplitQueue sq = own_plan(total, KT, min_steps, 512);
   bool own = true;
   int claim = 0;
-  for (WorkItem w = next_item(g, sq, total, KT, 16, 512, s_slot, own); w.tile >= 0;
-       w = i8::claimed_item(g, sq, claim, total, KT, 16, 512, s_slot, own)) {
+  for (WorkItem w = next_item(g, sq, total, KT, min_steps, 512, s_slot, own); w.tile >= 0;
+       w = i8::claimed_item(g, sq, claim, total, KT, min_steps, 512, s_slot, own)) {
     const int tid = opaque_tid(), lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     TileInfo ti = i8::decode(w.tile, tp, so, g.n_exp, g.n_tiles_n, BM);
@@ -637,8 +651,8 @@ static constexpr int kTileRows[] = {256, 128, 64, 32}, kTileCols[] = {256, 128, 
 // part and the tile's K steps (as many as its loop runs), or the stream of the weights where that takes
 // longer. The host does not know how the rows spread over the experts: `extra` m-tiles per expert stand
 // for ragged ends. The constants are fitted to 1000 products of 129 to 8192 rows, 1 to 64 experts (balanced
-// to skewed as (e + 1)^-1.3), N and K to 7168, each run on all four kinds: the kind so chosen takes 1.4 %
-// more than the best of the four on average (128-row tiles always: 10 %, any other kind always: 37 % or more).
+// to skewed as (e + 1)^-1.3), N and K to 7168, each run on all four kinds: the kind so chosen takes 1.8 %
+// more than the best of the four on average (128-row tiles always: 11 %, any other kind always: 37 %).
 static double tile_time(int kind, int n_rows, int n_exp, int cols, int K, int cus) {
   static constexpr double first[] = {25.0, 8.0, 8.2, 9.0};     // a single round's fixed part
   static constexpr double fix[] = {3.3, 4.8, 4.0, 7.6};        // that of each further round

@@ -34,9 +34,12 @@ TILES = {
     "few-8-small-grid-32-weight-rows": ([99], 7001, 528, "_few"),
     "m64": ([140], 770, 400, "_m64"),
     "m64-K-pieces": ([300], 300, 7152, "_m64"),
+    "m64-K-pieces-many-tiles": ([300], 900, 14416, "_m64"),
+    "m64-K-pieces-groups": ([70, 0, 3, 65], 700, 14416, "_m64"),
     "m64-one-step": ([333], 1000, 112, "_m64"),
     "m64-groups": ([70, 0, 3, 129, 64, 65], 515, 2032, "_m64"),
     "m128": ([1000], 4097, 1296, "_m128"),
+    "m128-K-pieces": ([1100], 1900, 14416, "_m128"),
     "m128-one-step": ([8000], 301, 48, "_m128"),
     "m128-groups": ([500, 0, 129, 1, 900, 128], 1500, 1424, "_m128"),
     "m256": ([5000], 3333, 784, ""),
